@@ -6,7 +6,7 @@ and each (block, kv head) of it one power-of-two scale 2^e, kept as the byte
 e + 127: the cached value is code * 2^e.
 
 write    The step's new K and V go into the cache.  A block written from its
-         first slot on takes the smallest exponent e in [-60, 60] with
+         first slot on takes the smallest exponent e in [-56, 56] with
          amax <= 448 * 2^e over its new finite elements; a block that already
          holds earlier tokens keeps the larger of that and its own, and when
          its exponent grows the codes of its earlier tokens are re-coded.
@@ -28,7 +28,7 @@ import torch
 own = False
 
 BLOCK = 16
-E_MIN, E_MAX, BIAS = -60, 60, 127
+E_MIN, E_MAX, BIAS = -56, 56, 127
 E4M3_MAX = 448.0
 DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
 WORKSPACE_BYTES = 256 << 20   # an engine's one workspace, kept for all its steps
