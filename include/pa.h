@@ -18,6 +18,11 @@
  *                      its own request's context, read through the block
  *                      table;
  *   pa_cache_write_ex / pa_attention_ex  the same over FP8 (E4M3) pools;
+ *   pa_cache_write_scaled / pa_attention_scaled / pa_copy_blocks_scaled  the
+ *                      same over FP8 pools whose scales follow the data, one
+ *                      per (block, kv head);
+ *   pa_cache_read      cached rows read back as 16-bit values, from pools of
+ *                      any kind;
  *
  * Conventions shared by every call:
  *   - Ownership: the caller allocates and owns every buffer.  The library
@@ -490,6 +495,146 @@ pa_status pa_attention_noalloc(const void *q, const void *key_cache, const void 
                                int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads,
                                int32_t head_dim, int32_t block_size, int32_t num_blocks,
                                float scale, pa_dtype dtype, void *out, pa_stream_t stream);
+
+/*
+ * Block-scaled pools -- FP8 (E4M3) pools with a scale per (block, kv head).
+ *
+ * "How vLLM Works Internally", section "FP8 KV Cache", with scales that the
+ * write takes from the data instead of one scale per pool that the caller
+ * must know beforehand.  Beside each pool (layout above, one byte per element)
+ * lies a table of scale bytes, uint8 [num_blocks][num_kv_heads], k_scales for
+ * the K pool and v_scales for the V pool: byte b stands for 2^(b - 127), and
+ *     cached value = E4M3 element * 2^(b - 127).
+ * pa_cache_write_scaled leaves bytes in [PA_SCALE_MIN, PA_SCALE_MAX]
+ * (exponents -56 .. 56); readers take a byte outside that range as its nearest
+ * end.  Scales are powers of two so that scaling never rounds: a cached value
+ * is one E4M3 rounding away from its source, and a block's scale can grow
+ * when a larger token joins it (see below).
+ */
+#define PA_SCALE_MIN 71
+#define PA_SCALE_MAX 183
+
+/*
+ * pa_cache_write_scaled -- the step's new K and V into block-scaled pools.
+ *
+ * For request r with n = query_start_loc[r+1] - query_start_loc[r] new tokens,
+ * at positions seq_lens[r] - n .. seq_lens[r] - 1 (flat tokens
+ * query_start_loc[r] ..), every block that holds one of these positions, each
+ * kv head of it, and K and V each on its own:
+ *   - amax is the largest finite magnitude among the block's new elements and
+ *     e_new the smallest exponent in -56 .. 56 with amax <= 448 * 2^e_new (56
+ *     where none is: such elements saturate);
+ *   - a block whose first new slot is 0 starts anew: e = e_new.  Any other
+ *     block holds earlier tokens in the slots before its first new one: e =
+ *     max(e_new, its scale's exponent), and if that is larger than its scale's
+ *     exponent e_old, the elements in those slots become E4M3(element *
+ *     2^(e_old - e)) -- exact unless the result is under E4M3's normal range;
+ *   - each new element x becomes E4M3(x * 2^-e), and the scale byte e + 127.
+ * E4M3() rounds to nearest, ties to even, and saturates at +-448 (infinities
+ * too); NaN stays NaN.  Slots behind the block's last new one, and everything
+ * else in the pools and tables, are left as they were.
+ *
+ * A step writes each block for one request only: a block that is shared and
+ * about to be written is copied first (pa_copy_blocks_scaled).  Where two
+ * requests of one call write the same block, the contents of that block are
+ * unspecified; every access still stays inside the pools.
+ *
+ * Arguments: key, value, kv_token_stride, the pools and dtype (of key/value)
+ * as pa_cache_write; k_scales, v_scales device tables as above; block_table,
+ * query_start_loc [num_reqs + 1] and seq_lens as pa_attention.  head_dim 64 or
+ * 128, block_size 16.  Flat tokens at or behind query_start_loc[num_reqs]
+ * write nothing; a request without new tokens writes nothing.
+ * Errors: PA_ERR_INVALID (negative sizes, NULL buffers, a stride below
+ * num_kv_heads * head_dim, a pool of 2^31 slots or more);
+ * PA_ERR_UNSUPPORTED (head_dim, block_size, key/value rows that are not 16-byte
+ * aligned, pools that are not 8-byte aligned, more than 50,000 requests).
+ * Data checks (that request or block is skipped): PA_CHECK_SEQ_LEN,
+ * PA_CHECK_LOGICAL_BLOCK, PA_CHECK_BLOCK_ID.
+ */
+pa_status pa_cache_write_scaled(const void *key, const void *value, int64_t kv_token_stride,
+                                void *key_cache, void *value_cache, uint8_t *k_scales,
+                                uint8_t *v_scales, const int32_t *block_table,
+                                int32_t max_blocks_per_req, const int32_t *query_start_loc,
+                                const int32_t *seq_lens, int32_t num_reqs, int32_t num_tokens,
+                                int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                int32_t num_blocks, pa_dtype dtype, pa_stream_t stream);
+
+/*
+ * pa_cache_read -- cached rows as contiguous 16-bit K and V.
+ *
+ * The read side of the cache outside attention: a context handed to another
+ * engine, to a dense kernel, or to a check.  For request r and i in
+ * [0, row_start_loc[r+1] - row_start_loc[r]), with p = first_positions[r] + i:
+ *   key_out[row_start_loc[r] + i]   = the cached K of position p, read through
+ *                                     block_table[r] and rounded once to dtype
+ *   value_out[row_start_loc[r] + i] = the cached V of position p
+ * Pools: cache_dtype == dtype copies; PA_FP8_E4M3 with k_scales and v_scales
+ * reads block-scaled pools (head_dim 64 or 128); PA_FP8_E4M3 without them reads
+ * element * *k_scale / * *v_scale (device scalars; NULL = 1.0).
+ *
+ * Arguments: first_positions [num_reqs] and row_start_loc [num_reqs + 1] device
+ * int32, row_start_loc[0] = 0 and not decreasing; num_rows the rows that
+ * key_out and value_out ([num_rows][num_kv_heads][head_dim], contiguous) have
+ * room for.  Rows at or behind row_start_loc[num_reqs] are left as they were,
+ * so a captured call can serve any total up to num_rows.
+ * Errors: PA_ERR_INVALID (negative sizes, NULL buffers, a cache_dtype that is
+ * neither dtype nor PA_FP8_E4M3, one scale table without the other, tables
+ * over 16-bit pools or beside k_scale / v_scale); PA_ERR_UNSUPPORTED
+ * (head_dim not a multiple of 8, or not 64 or 128 with tables; outputs or
+ * 16-bit pools not 16-byte aligned, FP8 pools not 8-byte aligned).
+ * Data checks (that row is left as it was): PA_CHECK_TOKEN_COUNT
+ * (row_start_loc[num_reqs] outside [0, num_rows]; the rows that fit are read),
+ * PA_CHECK_SEQ_LEN (a negative position), PA_CHECK_LOGICAL_BLOCK,
+ * PA_CHECK_BLOCK_ID.
+ */
+pa_status pa_cache_read(const void *key_cache, const void *value_cache, pa_dtype cache_dtype,
+                        const float *k_scale, const float *v_scale, const uint8_t *k_scales,
+                        const uint8_t *v_scales, const int32_t *block_table,
+                        int32_t max_blocks_per_req, const int32_t *first_positions,
+                        const int32_t *row_start_loc, int32_t num_reqs, int32_t num_rows,
+                        int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                        int32_t num_blocks, void *key_out, void *value_out, pa_dtype dtype,
+                        pa_stream_t stream);
+
+/*
+ * pa_copy_blocks_scaled -- pa_copy_blocks over block-scaled pools: the blocks'
+ * scale bytes go along, k_scales[dst] = k_scales[src] and v_scales likewise.
+ * Arguments and errors as pa_copy_blocks (dtype PA_FP8_E4M3), plus
+ * PA_ERR_INVALID for a NULL table with num_pairs > 0.  (A block that
+ * pa_zero_blocks cleared needs no scale: zero times any scale is zero, and a
+ * block written from its first slot on starts its scale anew.)
+ */
+pa_status pa_copy_blocks_scaled(void *key_cache, void *value_cache, uint8_t *k_scales,
+                                uint8_t *v_scales, const int32_t *src_blocks,
+                                const int32_t *dst_blocks, int32_t num_pairs, int32_t block_size,
+                                int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks,
+                                pa_stream_t stream);
+
+/*
+ * pa_attention_scaled -- pa_attention over block-scaled pools.
+ *
+ * Defined as pa_attention, the cached values being element * 2^(byte - 127)
+ * with the byte of the element's (block, kv head).  With ek, ev the exponents
+ * of the K and V scale of key j's block,
+ *     t_j = log2(e) * scale * 2^ek * (q . element_j) + ev,  m = max_j t_j,
+ *     out = sum_j 2^(t_j - m) * element_j / sum_j 2^(t_j - m) * 2^-ev:
+ * the weights 2^(t_j - m) enter the product with V's elements as f16, with 11
+ * significant bits relative to the heaviest key, and everything else is
+ * float32.  The matrix products run in f16 (E4M3 widens to it exactly; bf16 q
+ * is rounded to f16, exact inside f16's range), on the same two kernels and by
+ * the same rules as pa_attention.  Workspace as pa_attention
+ * (pa_attention_workspace_size), flags as pa_attention_ex.  Errors and data
+ * checks as pa_attention_ex, plus PA_ERR_INVALID for a NULL scale table.
+ */
+pa_status pa_attention_scaled(const void *q, const void *key_cache, const void *value_cache,
+                              const uint8_t *k_scales, const uint8_t *v_scales,
+                              const int32_t *block_table, int32_t max_blocks_per_req,
+                              const int32_t *query_start_loc, const int32_t *seq_lens,
+                              int32_t num_reqs, int32_t num_tokens, int32_t max_query_len,
+                              int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads,
+                              int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                              float scale, pa_dtype dtype, uint32_t flags, void *out,
+                              void *workspace, size_t workspace_bytes, pa_stream_t stream);
 
 /*
  * pa_get_status -- synchronise `stream`, then read and clear the current

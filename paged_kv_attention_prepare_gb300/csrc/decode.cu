@@ -81,6 +81,8 @@ struct Params {
     float qscale;         // softmax scale * log2(e)
     const float *k_scale; // FP8 pools: cached value = element * scale (device scalars)
     const float *v_scale;
+    const uint8_t *k_bscales;  // block-scaled E4M3 pools: [NB][Hkv] scale bytes
+    const uint8_t *v_bscales;
     unsigned int *status;
     int launch_pdl;       // host side: the split-K grid as a programmatic dependent of the grid before
     int launch_part;      // host side: 0 split-K grid and merge pass, 1 the grid only, 2 the merge only
@@ -88,6 +90,16 @@ struct Params {
 
 // Marker for an FP8 E4M3 cache element.
 struct Fp8E4M3 {};
+// The same with a power-of-two scale per (block, kv head).  K's exponent
+// multiplies its page's scores; V's joins the exponent of the softmax weight:
+// with t_j = s_j + ev(page of j) and m the reference max of the t_j, the
+// weights w_j = 2^(t_j - m) carry V's scale into PV, and the row sum takes
+// w_j * 2^-ev, so out = O / l as before and partials merge as before.  One
+// exponential per score, and the f16 weights keep their 11 bits whatever the
+// scales (2^(s_j - m) times a scale would underflow f16 in small blocks).
+struct Fp8Block {};
+template <typename TC>
+constexpr bool kIs8Bit = std::is_same<TC, Fp8E4M3>::value || std::is_same<TC, Fp8Block>::value;
 
 // Shared-memory layout of one cache page (16 slots of one kv head) as the
 // TMA writes it: rows of min(128, D * elt) bytes with the matching TMA
@@ -95,7 +107,7 @@ struct Fp8E4M3 {};
 // 16-row boxes, one per 128-byte half, stored back to back.
 template <typename TC, int D>
 struct Lay {
-    static constexpr int E = std::is_same<TC, Fp8E4M3>::value ? 1 : 2;  // bytes per element
+    static constexpr int E = kIs8Bit<TC> ? 1 : 2;     // bytes per element
     static constexpr int RB = D * E;                  // bytes per slot row
     static constexpr int SR = RB >= 128 ? 128 : RB;   // bytes per smem row
     static constexpr int NSUB = RB / SR;              // TMA boxes per page
@@ -118,6 +130,7 @@ struct Lay {
 // q's); f16 for an FP8 cache (E4M3 widens to f16 exactly).
 template <typename TQ, typename TC> struct MmaIn { using type = TC; };
 template <typename TQ> struct MmaIn<TQ, Fp8E4M3> { using type = __half; };
+template <typename TQ> struct MmaIn<TQ, Fp8Block> { using type = __half; };
 
 template <typename TC, int D, int RPI>
 struct Cfg {
@@ -150,6 +163,7 @@ struct Cfg {
     static constexpr int kComb = RPI * (kDC + 2);     // per warp: acc[row][kDC], m[row], l[row]
     static constexpr int kBytes = kStageBytes + kConsumerWarps * kComb * 4 +
                                   (2 * kStages + 2) * 8 + kCandidates * 8 + kQueue * 3 * 8 +
+                                  (std::is_same<TC, Fp8Block>::value ? kStages / 2 * kSP * 4 : 0) +
                                   1024;
 };
 
@@ -392,6 +406,10 @@ paged_decode_kernel(const __grid_constant__ Params p) {
     uint64_t *qfull = reinterpret_cast<uint64_t *>(cand + kCandidates);
     uint64_t *qempty = qfull + kQueue;
     long long *qitem = reinterpret_cast<long long *>(qempty + kQueue);
+    // block-scaled pools: per stage pair and page of its unit, the scale bytes
+    // (K's low, V's next)
+    constexpr bool kBlockScales = std::is_same<TC, Fp8Block>::value;
+    uint32_t *unit_scales = reinterpret_cast<uint32_t *>(qitem + kQueue);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // arrivals that release a stage: group items need all four warps
@@ -591,6 +609,14 @@ paged_decode_kernel(const __grid_constant__ Params p) {
                         blk = 0;
                     }
                 }
+                uint32_t sc = 0;
+                if constexpr (kBlockScales) {
+                    if (g0 + lane < npages) {
+                        const long long at = (long long)blk * p.Hkv + it.g;
+                        sc = (uint32_t)clamp_scale(__ldg(p.k_bscales + at)) |
+                             (uint32_t)clamp_scale(__ldg(p.v_bscales + at)) << 8;
+                    }
+                }
                 const int n = min(32, npages - g0);
                 for (int pu = 0; ok && pu < n; pu += kSP) {
                     const int cnt = min(kSP, n - pu);   // pages in this unit
@@ -601,6 +627,11 @@ paged_decode_kernel(const __grid_constant__ Params p) {
                     const uint32_t c = handed_to(w);
                     const uint32_t phase = (c / kPW) & 1u;
                     handed = (handed & ~(0xffu << (8 * w))) | (((c + 1) & 0xffu) << (8 * w));
+                    uint32_t us[kSP];
+                    if constexpr (kBlockScales) {
+#pragma unroll
+                        for (int sp = 0; sp < kSP; ++sp) us[sp] = __shfl_sync(0xffffffffu, sc, min(pu + sp, 31));
+                    }
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
                         const int stage = pair_stage<kPW>(w, c) + kv;
@@ -609,6 +640,14 @@ paged_decode_kernel(const __grid_constant__ Params p) {
                                 flag(p.status, PA_CHECK_TIMEOUT);
                                 ok = false;
                             } else {
+                                // read by the consumers before they release K
+                                if constexpr (kBlockScales) {
+                                    if (kv == 0) {
+#pragma unroll
+                                        for (int sp = 0; sp < kSP; ++sp)
+                                            unit_scales[(stage >> 1) * kSP + sp] = us[sp];
+                                    }
+                                }
                                 mbar_arrive_expect_tx(&full[stage], cnt * L::kPageBytes);
 #pragma unroll
                                 for (int sp = 0; sp < kSP; ++sp) {
@@ -793,10 +832,12 @@ paged_decode_kernel(const __grid_constant__ Params p) {
             bool have[kSP];
             int keyb[kSP];                 // first key of each page
             float sv[kSP][4];              // (key_a, row 2tq), (key_a, 2tq+1), (key_b, 2tq), (key_b, 2tq+1)
+            uint32_t psc[kSP];             // block-scaled pools: each page's scale bytes
 #pragma unroll
             for (int sp = 0; sp < kSP; ++sp) {
                 have[sp] = pu * kSP + sp < npages;
                 keyb[sp] = k0 + (pu * kSP + sp) * kPage;
+                psc[sp] = kBlockScales ? unit_scales[(stK >> 1) * kSP + sp] : 0u;
             }
             // ---- S^T = K Q^T for each page's 16 keys
 #pragma unroll
@@ -827,8 +868,15 @@ paged_decode_kernel(const __grid_constant__ Params p) {
                         }
                     }
                 }
+                if constexpr (kBlockScales) {
+                    const float kf = qs * __uint_as_float((psc[sp] & 0xffu) << 23);
+                    const float ev = (float)(int)((psc[sp] >> 8) - kScaleBias);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sv[sp][e] = have[sp] ? (sa[e] + sb[e]) * qs : -INFINITY;
+                    for (int e = 0; e < 4; ++e) sv[sp][e] = have[sp] ? fmaf(sa[e] + sb[e], kf, ev) : -INFINITY;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sv[sp][e] = have[sp] ? (sa[e] + sb[e]) * qs : -INFINITY;
+                }
             }
             const bool unit_visible = keyb[kSP - 1] + kPage - 1 <= lim_all && have[kSP - 1];
             // K is in registers now: its stage goes back to the producer half a
@@ -894,8 +942,14 @@ paged_decode_kernel(const __grid_constant__ Params p) {
                     pv[2] = m0 == -INFINITY ? 0.f : fast_exp2(sv[sp][2] - m0);
                     pv[3] = m1 == -INFINITY ? 0.f : fast_exp2(sv[sp][3] - m1);
                 }
-                l0 += pv[0] + pv[2];
-                l1 += pv[1] + pv[3];
+                if constexpr (kBlockScales) {   // the row sum is of the softmax weights alone
+                    const float iv = __uint_as_float((254u - (psc[sp] >> 8)) << 23);
+                    l0 = fmaf(pv[0] + pv[2], iv, l0);
+                    l1 = fmaf(pv[1] + pv[3], iv, l1);
+                } else {
+                    l0 += pv[0] + pv[2];
+                    l1 += pv[1] + pv[3];
+                }
                 const uint32_t h0 = Mma<TM>::pack(pv[0], pv[1]), h1 = Mma<TM>::pack(pv[2], pv[3]);
                 pb[sp][0] = movmatrix_trans(h0);
                 pb[sp][1] = movmatrix_trans(h1);
@@ -1192,7 +1246,7 @@ template <> __device__ __forceinline__ void fma_vec<float2>(float *o, float w, c
 
 // B: partial rows in flight per warp (fewer registers for short contexts)
 template <typename T, int D, int RPI, int WPH, int B>
-__global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const __grid_constant__ Params p) {
+static __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const __grid_constant__ Params p) {
     constexpr int DPL = D / 32;
     constexpr int kHeads = kMergeWarps / WPH;   // heads per CTA
     using V = typename MergeVec<DPL>::type;
@@ -1408,26 +1462,49 @@ pa_status dispatch_rpi(int rpi, Params &prm, long long grid, long long merge, bo
     }
 }
 
+template <typename TQ, typename TC>
+pa_status dispatch_dim(int D, int rpi, Params &prm, long long grid, long long merge, bool groups,
+                       cudaStream_t stream) {
+    return D == 128 ? dispatch_rpi<TQ, TC, 128>(rpi, prm, grid, merge, groups, stream)
+                    : dispatch_rpi<TQ, TC, 64>(rpi, prm, grid, merge, groups, stream);
+}
+
 template <typename TQ>
 pa_status dispatch_cache(bool fp8, int D, int rpi, Params &prm, long long grid, long long merge,
                          bool groups, cudaStream_t stream) {
-    if (fp8)
-        return D == 128 ? dispatch_rpi<TQ, Fp8E4M3, 128>(rpi, prm, grid, merge, groups, stream)
-                        : dispatch_rpi<TQ, Fp8E4M3, 64>(rpi, prm, grid, merge, groups, stream);
-    return D == 128 ? dispatch_rpi<TQ, TQ, 128>(rpi, prm, grid, merge, groups, stream)
-                    : dispatch_rpi<TQ, TQ, 64>(rpi, prm, grid, merge, groups, stream);
+    return fp8 ? dispatch_dim<TQ, Fp8E4M3>(D, rpi, prm, grid, merge, groups, stream)
+               : dispatch_dim<TQ, TQ>(D, rpi, prm, grid, merge, groups, stream);
 }
 
-// The fp16 instantiations compile in a translation unit of their own
-// (decode_fp16.cu includes this file with PA_DECODE_FP16_UNIT defined), in
-// parallel with the bf16 ones here.
+// Instantiations compile in translation units of their own, in parallel with
+// the bf16 ones here; each includes this file with its macro defined:
+// decode_fp16.cu (PA_DECODE_FP16_UNIT), and over block-scaled pools
+// decode_scaled.cu and decode_scaled_fp16.cu (PA_DECODE_SCALED_UNIT, the
+// query type).
 pa_status dispatch_fp16(bool fp8, int D, int rpi, Params &prm, long long grid, long long merge,
                         bool groups, cudaStream_t stream);
+template <typename TQ>
+pa_status dispatch_scaled(int D, int rpi, Params &prm, long long grid, long long merge,
+                          bool groups, cudaStream_t stream);
 #ifdef PA_DECODE_FP16_UNIT
 pa_status dispatch_fp16(bool fp8, int D, int rpi, Params &prm, long long grid, long long merge,
                         bool groups, cudaStream_t stream) {
     return dispatch_cache<__half>(fp8, D, rpi, prm, grid, merge, groups, stream);
 }
+#endif
+#ifdef PA_DECODE_SCALED_UNIT
+template <typename TQ>
+pa_status dispatch_scaled(int D, int rpi, Params &prm, long long grid, long long merge,
+                          bool groups, cudaStream_t stream) {
+    return dispatch_dim<TQ, Fp8Block>(D, rpi, prm, grid, merge, groups, stream);
+}
+template pa_status dispatch_scaled<PA_DECODE_SCALED_UNIT>(int, int, Params &, long long, long long,
+                                                          bool, cudaStream_t);
+#else
+extern template pa_status dispatch_scaled<__nv_bfloat16>(int, int, Params &, long long, long long,
+                                                         bool, cudaStream_t);
+extern template pa_status dispatch_scaled<__half>(int, int, Params &, long long, long long, bool,
+                                                  cudaStream_t);
 #endif
 
 // Rows per item: all heads of a kv group (at most 8, the register budget).
@@ -1453,7 +1530,7 @@ inline size_t round_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 }  // namespace decode
 
-#ifndef PA_DECODE_FP16_UNIT
+#if !defined(PA_DECODE_FP16_UNIT) && !defined(PA_DECODE_SCALED_UNIT)
 size_t decode_workspace_size(int32_t R, int32_t T, int32_t max_q, int32_t max_seq, int32_t Hq,
                              int32_t Hkv, int32_t D) {
     using namespace decode;
@@ -1484,6 +1561,8 @@ pa_status launch_decode(const AttnArgs &a, int tau, cudaStream_t stream) {
         return PA_ERR_CUDA;
     prm.k_scale = a.k_scale;
     prm.v_scale = a.v_scale;
+    prm.k_bscales = a.k_bscales;
+    prm.v_bscales = a.v_bscales;
     prm.q = a.q;
     prm.out = a.out;
     prm.bt = a.bt;
@@ -1550,10 +1629,14 @@ pa_status launch_decode(const AttnArgs &a, int tau, cudaStream_t stream) {
     const long long merge_splits = merge ? splits : 0;
     // group items need the partial slots (a merge pass) and the item queue
     const bool groups = (a.flags & PA_ATTN_SHARED_BLOCKS) && merge && a.ctrl;
+    if (a.k_bscales)
+        return a.dtype == PA_BF16
+                   ? dispatch_scaled<__nv_bfloat16>(a.D, rpi, prm, grid, merge_splits, groups, stream)
+                   : dispatch_scaled<__half>(a.D, rpi, prm, grid, merge_splits, groups, stream);
     return a.dtype == PA_BF16
                ? dispatch_cache<__nv_bfloat16>(fp8, a.D, rpi, prm, grid, merge_splits, groups, stream)
                : dispatch_fp16(fp8, a.D, rpi, prm, grid, merge_splits, groups, stream);
 }
-#endif  // PA_DECODE_FP16_UNIT
+#endif  // the bf16 unit
 
 }  // namespace pa

@@ -342,6 +342,114 @@ pa_status pa_cache_write(const void *key, const void *value, int64_t kv_token_st
                               reinterpret_cast<cudaStream_t>(stream));
 }
 
+pa_status pa_cache_write_scaled(const void *key, const void *value, int64_t kv_token_stride,
+                                void *key_cache, void *value_cache, uint8_t *k_scales,
+                                uint8_t *v_scales, const int32_t *block_table,
+                                int32_t max_blocks_per_req, const int32_t *query_start_loc,
+                                const int32_t *seq_lens, int32_t num_reqs, int32_t num_tokens,
+                                int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                int32_t num_blocks, pa_dtype dtype, pa_stream_t stream) {
+    if (num_reqs < 0 || num_tokens < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
+        num_blocks < 0 || max_blocks_per_req < 0 || (dtype != PA_BF16 && dtype != PA_FP16))
+        return PA_ERR_INVALID;
+    if (kv_token_stride < (int64_t)num_kv_heads * head_dim) return PA_ERR_INVALID;
+    if ((int64_t)num_blocks * block_size >= (int64_t)INT32_MAX) return PA_ERR_INVALID;
+    if (num_tokens > 0 && num_reqs > 0 &&
+        (!key || !value || !key_cache || !value_cache || !k_scales || !v_scales || !block_table ||
+         !query_start_loc || !seq_lens))
+        return PA_ERR_INVALID;
+    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (block_size != 16) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)num_kv_heads * head_dim > INT32_MAX / 2) return PA_ERR_UNSUPPORTED;
+    if (num_tokens == 0 || num_reqs == 0) return PA_OK;
+    if (!aligned(key, 16) || !aligned(value, 16) || kv_token_stride % 8 != 0 ||
+        !aligned(key_cache, 8) || !aligned(value_cache, 8))
+        return PA_ERR_UNSUPPORTED;
+    ScaledWriteArgs a{};
+    a.key = key;
+    a.value = value;
+    a.stride = kv_token_stride;
+    a.kc = static_cast<uint8_t *>(key_cache);
+    a.vc = static_cast<uint8_t *>(value_cache);
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.bt = block_table;
+    a.qsl = query_start_loc;
+    a.seq_lens = seq_lens;
+    a.R = num_reqs;
+    a.T = num_tokens;
+    a.MB = max_blocks_per_req;
+    a.NB = num_blocks;
+    a.Hkv = num_kv_heads;
+    return launch_cache_write_scaled(a, head_dim, dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_cache_read(const void *key_cache, const void *value_cache, pa_dtype cache_dtype,
+                        const float *k_scale, const float *v_scale, const uint8_t *k_scales,
+                        const uint8_t *v_scales, const int32_t *block_table,
+                        int32_t max_blocks_per_req, const int32_t *first_positions,
+                        const int32_t *row_start_loc, int32_t num_reqs, int32_t num_rows,
+                        int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                        int32_t num_blocks, void *key_out, void *value_out, pa_dtype dtype,
+                        pa_stream_t stream) {
+    if (num_reqs < 0 || num_rows < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
+        num_blocks < 0 || max_blocks_per_req < 0 || (dtype != PA_BF16 && dtype != PA_FP16) ||
+        (cache_dtype != dtype && cache_dtype != PA_FP8_E4M3))
+        return PA_ERR_INVALID;
+    // block scales: both tables or neither, only over E4M3 pools, and not
+    // beside a scale per pool
+    const bool fp8 = cache_dtype == PA_FP8_E4M3, block_scales = k_scales || v_scales;
+    if (block_scales && (!k_scales || !v_scales || !fp8 || k_scale || v_scale)) return PA_ERR_INVALID;
+    if ((int64_t)num_blocks * block_size >= (int64_t)INT32_MAX) return PA_ERR_INVALID;
+    if (num_rows > 0 && num_reqs > 0 && (!key_cache || !value_cache || !block_table ||
+                                         !first_positions || !row_start_loc || !key_out || !value_out))
+        return PA_ERR_INVALID;
+    if (head_dim % 8 != 0 || (block_scales && head_dim != 64 && head_dim != 128))
+        return PA_ERR_UNSUPPORTED;
+    if ((int64_t)num_kv_heads * head_dim > INT32_MAX / 16) return PA_ERR_UNSUPPORTED;
+    if (num_rows == 0 || num_reqs == 0) return PA_OK;
+    const size_t pool_align = fp8 ? 8 : 16;
+    if (!aligned(key_cache, pool_align) || !aligned(value_cache, pool_align) ||
+        !aligned(key_out, 16) || !aligned(value_out, 16))
+        return PA_ERR_UNSUPPORTED;
+    CacheReadArgs a{};
+    a.kc = key_cache;
+    a.vc = value_cache;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.bt = block_table;
+    a.first_pos = first_positions;
+    a.row_starts = row_start_loc;
+    a.R = num_reqs;
+    a.N = num_rows;
+    a.MB = max_blocks_per_req;
+    a.NB = num_blocks;
+    a.Hkv = num_kv_heads;
+    a.bs = block_size;
+    a.row = num_kv_heads * head_dim;
+    a.head_shift = head_dim == 128 ? 4 : 3;
+    a.key_out = key_out;
+    a.value_out = value_out;
+    return launch_cache_read(a, !fp8 ? 0 : block_scales ? 2 : 1, dtype,
+                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_copy_blocks_scaled(void *key_cache, void *value_cache, uint8_t *k_scales,
+                                uint8_t *v_scales, const int32_t *src_blocks,
+                                const int32_t *dst_blocks, int32_t num_pairs, int32_t block_size,
+                                int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks,
+                                pa_stream_t stream) {
+    if (num_pairs > 0 && (!k_scales || !v_scales)) return PA_ERR_INVALID;
+    const pa_status st = pa_copy_blocks(key_cache, value_cache, src_blocks, dst_blocks, num_pairs,
+                                        block_size, num_kv_heads, head_dim, num_blocks,
+                                        PA_FP8_E4M3, stream);
+    if (st != PA_OK) return st;
+    return launch_copy_scales(k_scales, v_scales, num_kv_heads, num_blocks, src_blocks, dst_blocks,
+                              num_pairs, reinterpret_cast<cudaStream_t>(stream));
+}
+
 size_t pa_attention_workspace_size(int32_t num_reqs, int32_t num_tokens, int32_t max_query_len,
                                    int32_t max_seq_len, int32_t num_q_heads,
                                    int32_t num_kv_heads, int32_t head_dim) {
@@ -367,6 +475,18 @@ pa_status pa_attention(const void *q, const void *key_cache, const void *value_c
                            workspace_bytes, stream);
 }
 
+static pa_status attention_checked(const void *q, const void *key_cache, const void *value_cache,
+                                   const int32_t *block_table, int32_t max_blocks_per_req,
+                                   const int32_t *query_start_loc, const int32_t *seq_lens,
+                                   int32_t num_reqs, int32_t num_tokens, int32_t max_query_len,
+                                   int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                                   float scale, pa_dtype dtype, pa_dtype cache_dtype,
+                                   const float *k_scale, const float *v_scale,
+                                   const uint8_t *k_scales, const uint8_t *v_scales,
+                                   uint32_t flags, void *out, void *workspace,
+                                   size_t workspace_bytes, pa_stream_t stream);
+
 pa_status pa_attention_ex(const void *q, const void *key_cache, const void *value_cache,
                           const int32_t *block_table, int32_t max_blocks_per_req,
                           const int32_t *query_start_loc, const int32_t *seq_lens,
@@ -376,6 +496,41 @@ pa_status pa_attention_ex(const void *q, const void *key_cache, const void *valu
                           pa_dtype dtype, pa_dtype cache_dtype, const float *k_scale,
                           const float *v_scale, uint32_t flags, void *out, void *workspace,
                           size_t workspace_bytes, pa_stream_t stream) {
+    return attention_checked(q, key_cache, value_cache, block_table, max_blocks_per_req,
+                             query_start_loc, seq_lens, num_reqs, num_tokens, max_query_len,
+                             max_seq_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                             num_blocks, scale, dtype, cache_dtype, k_scale, v_scale, nullptr,
+                             nullptr, flags, out, workspace, workspace_bytes, stream);
+}
+
+pa_status pa_attention_scaled(const void *q, const void *key_cache, const void *value_cache,
+                              const uint8_t *k_scales, const uint8_t *v_scales,
+                              const int32_t *block_table, int32_t max_blocks_per_req,
+                              const int32_t *query_start_loc, const int32_t *seq_lens,
+                              int32_t num_reqs, int32_t num_tokens, int32_t max_query_len,
+                              int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads,
+                              int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                              float scale, pa_dtype dtype, uint32_t flags, void *out,
+                              void *workspace, size_t workspace_bytes, pa_stream_t stream) {
+    if (num_tokens > 0 && num_reqs > 0 && (!k_scales || !v_scales)) return PA_ERR_INVALID;
+    return attention_checked(q, key_cache, value_cache, block_table, max_blocks_per_req,
+                             query_start_loc, seq_lens, num_reqs, num_tokens, max_query_len,
+                             max_seq_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                             num_blocks, scale, dtype, PA_FP8_E4M3, nullptr, nullptr, k_scales,
+                             v_scales, flags, out, workspace, workspace_bytes, stream);
+}
+
+static pa_status attention_checked(const void *q, const void *key_cache, const void *value_cache,
+                                   const int32_t *block_table, int32_t max_blocks_per_req,
+                                   const int32_t *query_start_loc, const int32_t *seq_lens,
+                                   int32_t num_reqs, int32_t num_tokens, int32_t max_query_len,
+                                   int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                                   float scale, pa_dtype dtype, pa_dtype cache_dtype,
+                                   const float *k_scale, const float *v_scale,
+                                   const uint8_t *k_scales, const uint8_t *v_scales,
+                                   uint32_t flags, void *out, void *workspace,
+                                   size_t workspace_bytes, pa_stream_t stream) {
     if (flags & ~PA_ATTN_SHARED_BLOCKS) return PA_ERR_INVALID;
     if (num_reqs < 0 || num_tokens < 0 || max_query_len < 0 || max_seq_len < 0 ||
         num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
@@ -416,6 +571,8 @@ pa_status pa_attention_ex(const void *q, const void *key_cache, const void *valu
     a.cache_dtype = cache_dtype;
     a.k_scale = cache_dtype == PA_FP8_E4M3 ? k_scale : nullptr;
     a.v_scale = cache_dtype == PA_FP8_E4M3 ? v_scale : nullptr;
+    a.k_bscales = k_scales;
+    a.v_bscales = v_scales;
     a.out = out;
     a.flags = flags;
     // The workspace starts with a small control block (the kernels' item

@@ -68,6 +68,45 @@ pa_status launch_cache_write_fp8(const void *key, const void *value, int64_t str
                                  int32_t row_elems, int64_t num_slots, pa_dtype src,
                                  const float *k_scale, const float *v_scale, cudaStream_t stream);
 
+// Pools with a scale per (block, kv head): a byte holds e + kScaleBias, the
+// cached value is code * 2^e.  e stays within +-56: then the weights that two
+// blocks of one context can get in the attention kernels (softmax weight *
+// 2^e) differ by at most 2^112 through the scales, inside float's range with
+// room for the lazily moved reference max.
+constexpr int kScaleBias = 127;
+constexpr int kScaleMinExp = PA_SCALE_MIN - kScaleBias;
+constexpr int kScaleMaxExp = PA_SCALE_MAX - kScaleBias;
+static_assert(kScaleMinExp == -56 && kScaleMaxExp == 56, "scale exponents");
+
+struct ScaledWriteArgs {
+    const void *key, *value;   // [T] rows of Hkv*D elements, `stride` elements apart
+    int64_t stride;
+    uint8_t *kc, *vc;          // pools [NB*16][Hkv][D]
+    uint8_t *k_scales, *v_scales;  // [NB][Hkv]
+    const int32_t *bt, *qsl, *seq_lens;
+    int32_t R, T, MB, NB, Hkv;
+    unsigned int *status;
+};
+pa_status launch_cache_write_scaled(ScaledWriteArgs a, int32_t D, pa_dtype dtype,
+                                    cudaStream_t stream);
+
+struct CacheReadArgs {
+    const void *kc, *vc;
+    const uint8_t *k_scales, *v_scales;  // [NB][Hkv] (block-scaled pools)
+    const float *k_scale, *v_scale;      // one scale per pool (NULL = 1)
+    const int32_t *bt, *first_pos, *row_starts;
+    int32_t R, N, MB, NB, Hkv, bs;
+    int32_t row;                         // elements per row (Hkv*D)
+    int32_t head_shift;                  // block-scaled pools: log2(D / 8)
+    void *key_out, *value_out;
+    unsigned int *status;
+};
+// pool 0: 16-bit, 1: E4M3 with one scale, 2: E4M3 with block scales.
+pa_status launch_cache_read(CacheReadArgs a, int pool, pa_dtype dtype, cudaStream_t stream);
+pa_status launch_copy_scales(uint8_t *k_scales, uint8_t *v_scales, int32_t Hkv, int32_t NB,
+                             const int32_t *src, const int32_t *dst, int32_t n,
+                             cudaStream_t stream);
+
 struct AttnArgs {
     const void *q;
     const void *kc, *vc;
@@ -80,6 +119,8 @@ struct AttnArgs {
     pa_dtype cache_dtype;  // the pools: dtype, or PA_FP8_E4M3
     const float *k_scale;  // FP8 pools: device scalars (NULL = 1)
     const float *v_scale;
+    const uint8_t *k_bscales;  // E4M3 pools with a scale per (block, kv head): [NB][Hkv]
+    const uint8_t *v_bscales;  // (NULL: one scale per pool)
     void *out;
     void *ws;              // decode partials (after the control block)
     size_t ws_bytes;
@@ -312,6 +353,32 @@ __device__ __forceinline__ uint2 quantize8_e4m3(const uint4 src, float scale) {
         out[e >> 1] |= (q & 0xffffu) << (16 * (e & 1));
     }
     return make_uint2(out[0], out[1]);
+}
+
+// Scale bytes of block-scaled pools.  Bytes outside the range that the write
+// leaves are read as its nearest end.
+__host__ __device__ __forceinline__ int clamp_scale(int byte) {
+    const int lo = kScaleBias + kScaleMinExp, hi = kScaleBias + kScaleMaxExp;
+    return byte < lo ? lo : byte > hi ? hi : byte;
+}
+// 2^e for e in [-126, 127].
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+__device__ __forceinline__ float scale_value(uint8_t byte) { return pow2f(clamp_scale(byte) - kScaleBias); }
+
+// Eight E4M3 codes (code 0 in the low byte) times `scale`, rounded once to
+// 16-bit elements.
+template <typename T>
+__device__ __forceinline__ uint4 dequantize8(const uint2 c, float scale) {
+    const uint32_t w[2] = {c.x, c.y};
+    uint32_t out[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+            (__nv_fp8x2_storage_t)((w[e >> 1] >> (16 * (e & 1))) & 0xffffu), __NV_E4M3);
+        const float2 v = __half22float2(__half2(h));
+        out[e] = Elt<T>::pack2(v.x * scale, v.y * scale);
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 }  // namespace pa

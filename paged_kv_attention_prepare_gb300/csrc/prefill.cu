@@ -41,6 +41,15 @@
 // more warps (10, 11) widen the tile into the f16 layout, row by row, and
 // only then signal the tile full.  K's scale joins the softmax scale, V's
 // scales the output.
+//
+// Block-scaled FP8 pools (a power of two per block and kv head): the tile is
+// widened and multiplied unscaled; the scales act where the scores are already
+// in registers.  A page's 16 score columns take its K factor in the same
+// multiply-add as the softmax scale, and its V exponent ev in the addend: the
+// weights w = 2^(s + ev - m), m the running max of s + ev, carry V's scale
+// into PV, and the row sum takes a page's weights times 2^-ev.  The producer
+// leaves the three numbers of each page in shared memory, one copy per V
+// stage.
 #include <cudaTypedefs.h>
 
 #include <climits>
@@ -91,6 +100,7 @@ struct Params {
     int tau;        // requests with more than tau query tokens are handled here
     float qscale;   // softmax scale * log2(e)
     const float *k_scale, *v_scale;   // FP8 pools (device scalars; NULL = 1)
+    const uint8_t *k_bscales, *v_bscales;   // block-scaled FP8 pools: [NB][Hkv] scale bytes
     unsigned int *item_counter;       // zeroed before launch: items are taken in order
                                       // as CTAs free up (NULL: fixed snake order)
     // bf16 pools: V of the prefill requests widened to f16 once per call by
@@ -117,6 +127,10 @@ struct Cfg {
     static constexpr int kLandBytes = kBN * 64;
     static constexpr int kLandOffset = 2 * kQBytes + 4 * kTileBytes + 1024;
     static constexpr int kSmemF8Land = kLandOffset + 4 * kLandBytes + 1024;
+    // block-scaled pools: each page's (K factor, V exponent, 2^-ev), per V
+    // stage, right after the control block (in the staging area's alignment
+    // gap at head_dim 64)
+    static constexpr int kScaleBytes = 2 * kPagesPerTile * 16;
     // TMEM columns: S_A 0, O_A 128, S_B 256, O_B 384
     __device__ static constexpr uint32_t col_s(int slot) { return (uint32_t)slot * 256; }
     __device__ static constexpr uint32_t col_o(int slot) { return (uint32_t)slot * 256 + 128; }
@@ -139,7 +153,8 @@ enum {
     B_IEMPTY = B_IFULL + 4,       // [kQueue] entry read by every other warp
     B_SPLITREQ = B_IEMPTY + 4,    // [2] per slot: the MMA warp asks for P as bf16 pairs
     B_SPLITDONE = B_SPLITREQ + 2, // [2] per slot: P rewritten (one arrive per softmax warp)
-    B_COUNT = B_SPLITDONE + 2
+    B_PSCALE = B_SPLITDONE + 2,   // [2] per V stage: the tile's page scales written
+    B_COUNT = B_PSCALE + 2
 };
 constexpr int kQueue = 4;         // items the producer may run ahead
 
@@ -539,7 +554,8 @@ __device__ __noinline__ bool pv_with_bf16_halves(uint64_t *req, uint64_t *done, 
     return true;
 }
 
-template <typename T, int D, bool F8>
+// F8: FP8 pools; BS: with a scale per (block, kv head).
+template <typename T, int D, bool F8, bool BS>
 __global__ void __launch_bounds__(threads_for(Conv<T, F8>::kAny), 1)
 paged_prefill_kernel(const __grid_constant__ Params p) {
     using C = Cfg<D>;
@@ -575,6 +591,9 @@ paged_prefill_kernel(const __grid_constant__ Params p) {
     // bf16 pools: per V stage, 1 when the tile came widened (no conversion)
     volatile int *v_src = split_fmt + 2;        // [3]
     static_assert(B_COUNT * 8 + (2 + kQueue + 2 * 3 + 2 + 3) * 4 <= 512, "control block");
+    static_assert(!BS || F8, "block scales belong to FP8 pools");
+    // block-scaled pools: [2 V stages][pages of a tile] (K factor, V exponent, 2^-ev)
+    float4 *page_scales = reinterpret_cast<float4 *>(reinterpret_cast<unsigned char *>(bar) + 512);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // A grid launched after this one as a programmatic dependent (the
@@ -711,6 +730,7 @@ paged_prefill_kernel(const __grid_constant__ Params p) {
                 const int npg = min(kPagesPerTile, ctx_pages - pg0);
                 int blk = 0;
                 uint32_t wfl = 0;
+                uint32_t kb = 0, vb = 0;   // block-scaled pools: the page's scale bytes
                 if (lane < npg) {
                     blk = row[pg0 + lane];
                     if (kConvV && woff >= 0)
@@ -718,6 +738,11 @@ paged_prefill_kernel(const __grid_constant__ Params p) {
                     if (blk < 0 || blk >= p.NB) {
                         flag(p.status, PA_CHECK_BLOCK_ID);
                         blk = 0;
+                    }
+                    if constexpr (BS) {
+                        const long long at = (long long)blk * p.Hkv + it.g;
+                        kb = __ldg(p.k_bscales + at);
+                        vb = __ldg(p.v_bscales + at);
                     }
                 }
                 // V of this tile from the widened copy: one 128-token box
@@ -749,6 +774,20 @@ paged_prefill_kernel(const __grid_constant__ Params p) {
                     }
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                     if (!ok) break;
+                    if constexpr (BS) {
+                        // With V's stage free, the softmax is done with the
+                        // scales of the tile two back.
+                        if (kv) {
+                            if (lane < kPagesPerTile) {
+                                const int ek = clamp_scale((int)kb) - kScaleBias;
+                                const int ev = clamp_scale((int)vb) - kScaleBias;
+                                page_scales[st * kPagesPerTile + lane] =
+                                    make_float4(p.qscale * pow2f(ek), (float)ev, pow2f(-ev), 0.f);
+                            }
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bar[B_PSCALE + st]);
+                        }
+                    }
                     if (kConvV && kv && vw) {
                         if (lane == 0) {
 #pragma unroll
@@ -1146,6 +1185,88 @@ paged_prefill_kernel(const __grid_constant__ Params p) {
                     }
                     tmem_wait_st();
                     l += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+                } else if constexpr (BS) {
+                    // Block-scaled pools: the two passes below, page by page.
+                    const int sst = (int)((t0 + j) & 1);
+                    if (!mbar_wait_warp(&bar[B_PSCALE + sst], (uint32_t)(((t0 + j) >> 1) & 1))) {
+                        ok = false;
+                        break;
+                    }
+                    const float4 *ps = page_scales + sst * kPagesPerTile;
+                    float mx = -INFINITY;
+    #pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        uint32_t r[64];
+                        tmem_ld32(colS + hh * 64, *reinterpret_cast<uint32_t (*)[32]>(r));
+                        tmem_ld32(colS + hh * 64 + 32, *reinterpret_cast<uint32_t (*)[32]>(r + 32));
+                        tmem_wait_ld();
+                        if (!full_tile) {
+    #pragma unroll
+                            for (int k = 0; k < 64; ++k)
+                                if (key0 + hh * 64 + k > pos) r[k] = 0xff800000u;
+                        }
+    #pragma unroll
+                        for (int pg = 0; pg < 4; ++pg) {
+                            const float4 sc = ps[hh * 4 + pg];
+                            float m2[2] = {-INFINITY, -INFINITY};
+    #pragma unroll
+                            for (int k = 0; k < 16; k += 2)
+                                m2[(k >> 1) & 1] =
+                                    fmaxf(m2[(k >> 1) & 1], fmaxf(__uint_as_float(r[16 * pg + k]),
+                                                                  __uint_as_float(r[16 * pg + k + 1])));
+                            mx = fmaxf(mx, fmaf(fmaxf(m2[0], m2[1]), sc.x, sc.y));
+                        }
+                    }
+                    const bool need = mx > m_ref + kRescaleThreshold;
+                    if (j > 0 && __any_sync(0xffffffffu, need)) {
+                        // O holds PV of tiles < j, all complete: S_j's commit (waited
+                        // above) covers every MMA issued before it.  Rescale.
+                        const float alpha = need ? fast_exp2(m_ref - mx) : 1.f;
+    #pragma unroll
+                        for (int cc = 0; cc < D; cc += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(colO + cc, o);
+                            tmem_wait_ld();
+    #pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st32(colO + cc, o);
+                        }
+                        tmem_wait_st();
+                        if (need) l *= alpha;
+                    }
+                    if (need) m_ref = mx;
+    #pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        uint32_t r[64];
+                        tmem_ld32(colS + hh * 64, *reinterpret_cast<uint32_t (*)[32]>(r));
+                        tmem_ld32(colS + hh * 64 + 32, *reinterpret_cast<uint32_t (*)[32]>(r + 32));
+                        tmem_wait_ld();
+                        if (!full_tile) {
+    #pragma unroll
+                            for (int k = 0; k < 64; ++k)
+                                if (key0 + hh * 64 + k > pos) r[k] = 0xff800000u;
+                        }
+                        uint32_t w[32];
+    #pragma unroll
+                        for (int pg = 0; pg < 4; ++pg) {
+                            const float4 sc = ps[hh * 4 + pg];
+                            const float2 kf = make_float2(sc.x, sc.x);
+                            const float2 add = make_float2(sc.y - m_ref, sc.y - m_ref);
+                            float2 acc = make_float2(0.f, 0.f);
+    #pragma unroll
+                            for (int e = 8 * pg; e < 8 * pg + 8; ++e) {
+                                float2 y = __ffma2_rn(make_float2(__uint_as_float(r[2 * e]),
+                                                                  __uint_as_float(r[2 * e + 1])), kf, add);
+                                y.x = fast_exp2(y.x);
+                                y.y = fast_exp2(y.y);
+                                acc = __fadd2_rn(acc, y);
+                                w[e] = Elt<__half>::pack2(y.x, y.y);
+                            }
+                            l = fmaf(acc.x + acc.y, sc.z, l);
+                        }
+                        tmem_st32(colS + hh * 64, w);
+                    }
+                    tmem_wait_st();
                 } else {
                     // FP8 pools: two passes over the scores (row max, then P).
                     // The one-pass form above measured slower here when scores
@@ -1322,17 +1443,20 @@ bool encode_sw128(CUtensorMap *map, const void *ptr, uint64_t d0, uint64_t d1, u
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D, bool F8>
+template <typename T, int D, bool F8, bool BS = false>
 pa_status launch_typed(const Params &prm, long long items, long long max_ctas, bool pdl,
                        cudaStream_t stream) {
     using C = Cfg<D>;
-    constexpr int kSmem = (F8 && D == 64) ? C::kSmemF8Land : C::smem(Conv<T, F8>::kV ? 3 : 2);
+    constexpr int kSmem = (F8 && D == 64) ? C::kSmemF8Land
+                                          : C::smem(Conv<T, F8>::kV ? 3 : 2) + (BS ? C::kScaleBytes : 0);
+    static_assert(2 * C::kQBytes + 4 * C::kTileBytes + 512 + C::kScaleBytes <= C::kLandOffset,
+                  "the page scales fit before the staging area");
     static_assert(kSmem <= 232448, "shared memory per CTA");
     static bool configured[64] = {};
     int dev = 0;
     PA_TRY_CUDA(cudaGetDevice(&dev));
     if (dev >= 64 || !configured[dev]) {
-        PA_TRY_CUDA(cudaFuncSetAttribute(paged_prefill_kernel<T, D, F8>,
+        PA_TRY_CUDA(cudaFuncSetAttribute(paged_prefill_kernel<T, D, F8, BS>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
         if (dev < 64) configured[dev] = true;
     }
@@ -1350,9 +1474,9 @@ pa_status launch_typed(const Params &prm, long long items, long long max_ctas, b
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        PA_TRY_CUDA(cudaLaunchKernelEx(&cfg, paged_prefill_kernel<T, D, F8>, prm));
+        PA_TRY_CUDA(cudaLaunchKernelEx(&cfg, paged_prefill_kernel<T, D, F8, BS>, prm));
     } else {
-        paged_prefill_kernel<T, D, F8><<<(int)grid, threads_for(Conv<T, F8>::kAny), kSmem, stream>>>(prm);
+        paged_prefill_kernel<T, D, F8, BS><<<(int)grid, threads_for(Conv<T, F8>::kAny), kSmem, stream>>>(prm);
         PA_TRY_CUDA(cudaGetLastError());
     }
     note_launch();
@@ -1364,6 +1488,12 @@ pa_status launch_kind(const AttnArgs &a, const Params &prm, long long items, lon
                       bool pdl, cudaStream_t stream) {
     const bool f8 = a.cache_dtype == PA_FP8_E4M3;
     const bool bf16 = a.dtype == PA_BF16;
+    if (a.k_bscales && a.D == 128)
+        return bf16 ? launch_typed<__nv_bfloat16, 128, true, true>(prm, items, max_ctas, pdl, stream)
+                    : launch_typed<__half, 128, true, true>(prm, items, max_ctas, pdl, stream);
+    if (a.k_bscales)
+        return bf16 ? launch_typed<__nv_bfloat16, 64, true, true>(prm, items, max_ctas, pdl, stream)
+                    : launch_typed<__half, 64, true, true>(prm, items, max_ctas, pdl, stream);
     if (f8 && a.D == 128)
         return bf16 ? launch_typed<__nv_bfloat16, 128, true>(prm, items, max_ctas, pdl, stream)
                     : launch_typed<__half, 128, true>(prm, items, max_ctas, pdl, stream);
@@ -1534,6 +1664,8 @@ static pa_status build(const AttnArgs &a, int tau, cudaStream_t stream, Params &
         return PA_ERR_CUDA;
     prm.k_scale = a.k_scale;
     prm.v_scale = a.v_scale;
+    prm.k_bscales = a.k_bscales;
+    prm.v_bscales = a.v_bscales;
     // items in order as CTAs free up (the caller zeroed the counter)
     prm.item_counter = a.ctrl ? a.ctrl + kCtrlPrefillCounter : nullptr;
     prm.out = a.out;
