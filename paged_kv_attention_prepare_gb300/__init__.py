@@ -18,6 +18,7 @@ Functions carry the C names: ``pa_prepare_inputs``, ``pa_prepare_inputs_ex``,
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import threading
 
@@ -25,6 +26,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpa.so")
+NATIVE_PATH = os.path.join(_HERE, "_native.so")
 
 PA_OK, PA_ERR_INVALID, PA_ERR_CUDA, PA_ERR_UNSUPPORTED = 0, 1, 2, 3
 PA_ERR_DEVICE_CHECK, PA_ERR_TIMEOUT, PA_ERR_WORKSPACE = 4, 5, 6
@@ -43,6 +45,7 @@ _DTYPES = {torch.bfloat16: PA_BF16, torch.float16: PA_FP16}
 _FP8_POOL = {torch.uint8, torch.float8_e4m3fn}
 _lock = threading.Lock()
 _lib = None
+_native = None
 
 
 class PAError(RuntimeError):
@@ -388,42 +391,18 @@ def pa_attention_noalloc(q, key_cache, value_cache, block_table, query_start_loc
     _check(rc, "pa_attention_noalloc")
 
 
-def _on_device(tensors):
-    """Every tensor of a call on one CUDA device; returns that device."""
-    dev = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the tensors before it on {dev}")
-    return dev
-
-
-def _scaled_pools(key_cache, value_cache, k_scales, v_scales):
-    """(num_blocks, block_size, num_kv_heads, head_dim) of block-scaled pools
-    and their tables."""
-    nb, bs, hkv, d, dt = _pools(key_cache, value_cache)
-    if dt != PA_FP8_E4M3:
-        raise TypeError("block scales belong to FP8 pools (uint8/float8_e4m3fn)")
-    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-        _dev(t, name, torch.uint8)
-        if tuple(t.shape) != (nb, hkv):
-            raise ValueError(f"{name} must be [{nb}, {hkv}] (blocks, kv heads), got {tuple(t.shape)}")
-    return nb, bs, hkv, d
-
-
-def _batch(block_table, starts, lens, starts_name, lens_name):
-    """Number of requests of a batch whose index tensors agree on it."""
-    r = lens.shape[0]
-    if lens.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != r \
-            or tuple(starts.shape) != (r + 1,):
-        raise ValueError(f"block_table [R, MB], {starts_name} [R + 1] and {lens_name} [R] must "
-                         "agree on R")
-    return r
+def native():
+    """The native half of the binding (``csrc/binding.cpp``), which checks and
+    marshals the calls below; raises if it has not been built."""
+    global _native
+    if _native is None:
+        lib()
+        if not os.path.exists(NATIVE_PATH):
+            raise RuntimeError(
+                f"{NATIVE_PATH} is missing: build the CUDA library first "
+                "(python -m paged_kv_attention_prepare_gb300.builder)")
+        _native = importlib.import_module("._native", __name__)
+    return _native
 
 
 def pa_cache_write_scaled(key, value, key_cache, value_cache, k_scales, v_scales, block_table,
@@ -431,32 +410,14 @@ def pa_cache_write_scaled(key, value, key_cache, value_cache, k_scales, v_scales
     """The step's key/value [T, Hkv, D] (token stride may exceed Hkv*D) into
     FP8 pools [NB, 16, Hkv, D] with scale bytes ``k_scales``/``v_scales`` uint8
     [NB, Hkv] (cached value = element * 2^(byte - 127)): each block's scale
-    follows its tokens, and a block that a larger token joins is re-coded."""
-    with torch.cuda.device(_on_device({
-            "key": key, "value": value, "key_cache": key_cache, "value_cache": value_cache,
-            "k_scales": k_scales, "v_scales": v_scales, "block_table": block_table,
-            "query_start_loc": query_start_loc, "seq_lens": seq_lens})):
-        nb, bs, hkv, d = _scaled_pools(key_cache, value_cache, k_scales, v_scales)
-        dt = _DTYPES.get(key.dtype)
-        if dt is None or value.dtype != key.dtype:
-            raise TypeError("key and value must share a bf16/fp16 dtype")
-        if key.dim() != 3 or key.shape[1:] != (hkv, d) or value.shape != key.shape:
-            raise ValueError(f"key and value must both be [T, {hkv}, {d}]")
-        T = key.shape[0]
-        for t in (key, value) if T else ():
-            if (hkv > 1 and t.stride(1) != d) or t.stride(2) != 1:
-                raise ValueError("key/value rows must be [Hkv, D]-contiguous")
-        if T > 1 and value.stride(0) != key.stride(0):
-            raise ValueError("key and value must have equal token strides")
-        R = _batch(block_table, query_start_loc, seq_lens, "query_start_loc", "seq_lens")
-        rc = lib().pa_cache_write_scaled(
-            _dev(key, "key", contiguous=False), _dev(value, "value", contiguous=False),
-            int(key.stride(0)) if T > 1 else hkv * d, _dev(key_cache, "key_cache"),
-            _dev(value_cache, "value_cache"), _dev(k_scales, "k_scales"),
-            _dev(v_scales, "v_scales"), _dev(block_table, "block_table", torch.int32),
-            block_table.shape[1], _dev(query_start_loc, "query_start_loc", torch.int32),
-            _dev(seq_lens, "seq_lens", torch.int32), R, T, hkv, d, bs, nb, dt, _stream(stream))
-    _check(rc, "pa_cache_write_scaled")
+    follows its tokens, and a block that a larger token joins is re-coded.
+    ``block_table`` [R, MB], ``query_start_loc`` [R + 1] and ``seq_lens`` [R]
+    as for attention."""
+    rc = (_native or native()).cache_write_scaled(
+        key, value, key_cache, value_cache, k_scales, v_scales, block_table, query_start_loc,
+        seq_lens, stream)
+    if rc != PA_OK:
+        raise PAError(rc, "pa_cache_write_scaled")
 
 
 def pa_cache_read(key_cache, value_cache, block_table, first_positions, row_start_loc, key_out,
@@ -466,49 +427,21 @@ def pa_cache_read(key_cache, value_cache, block_table, first_positions, row_star
     request r.  Pools of the outputs' dtype are copied; FP8 pools read element *
     2^(byte - 127) with ``k_scales``/``v_scales`` (uint8 [NB, Hkv]), otherwise
     element * ``k_scale`` / ``v_scale`` (one-element float32, None = 1.0)."""
-    with torch.cuda.device(_on_device({
-            "key_cache": key_cache, "value_cache": value_cache, "block_table": block_table,
-            "first_positions": first_positions, "row_start_loc": row_start_loc,
-            "key_out": key_out, "value_out": value_out, "k_scales": k_scales,
-            "v_scales": v_scales, "k_scale": k_scale, "v_scale": v_scale})):
-        nb, bs, hkv, d, cdt = _pools(key_cache, value_cache)
-        if k_scales is not None or v_scales is not None:
-            _scaled_pools(key_cache, value_cache, k_scales, v_scales)
-        dt = _DTYPES.get(key_out.dtype)
-        if dt is None or value_out.dtype != key_out.dtype:
-            raise TypeError("key_out and value_out must share a bf16/fp16 dtype")
-        if key_out.dim() != 3 or key_out.shape[1:] != (hkv, d) or value_out.shape != key_out.shape:
-            raise ValueError(f"key_out and value_out must both be [N, {hkv}, {d}]")
-        R = _batch(block_table, row_start_loc, first_positions, "row_start_loc", "first_positions")
-        opt = lambda t, name: None if t is None else _dev(t, name)  # noqa: E731
-        rc = lib().pa_cache_read(
-            _dev(key_cache, "key_cache"), _dev(value_cache, "value_cache"), cdt,
-            _scale_ptr(k_scale, "k_scale"), _scale_ptr(v_scale, "v_scale"),
-            opt(k_scales, "k_scales"), opt(v_scales, "v_scales"),
-            _dev(block_table, "block_table", torch.int32), block_table.shape[1],
-            _dev(first_positions, "first_positions", torch.int32),
-            _dev(row_start_loc, "row_start_loc", torch.int32), R, key_out.shape[0], hkv, d, bs, nb,
-            _dev(key_out, "key_out"), _dev(value_out, "value_out"), dt, _stream(stream))
-    _check(rc, "pa_cache_read")
+    rc = (_native or native()).cache_read(
+        key_cache, value_cache, block_table, first_positions, row_start_loc, key_out, value_out,
+        k_scales, v_scales, k_scale, v_scale, stream)
+    if rc != PA_OK:
+        raise PAError(rc, "pa_cache_read")
 
 
 def pa_copy_blocks_scaled(key_cache, value_cache, k_scales, v_scales, src_blocks, dst_blocks,
                           stream=None):
     """Copy-on-write over block-scaled FP8 pools: block dst_blocks[i] of both
     pools, and its scale bytes, become those of block src_blocks[i]."""
-    with torch.cuda.device(_on_device({
-            "key_cache": key_cache, "value_cache": value_cache, "k_scales": k_scales,
-            "v_scales": v_scales, "src_blocks": src_blocks, "dst_blocks": dst_blocks})):
-        nb, bs, hkv, d = _scaled_pools(key_cache, value_cache, k_scales, v_scales)
-        if src_blocks.shape != dst_blocks.shape or src_blocks.dim() != 1:
-            raise ValueError("src_blocks and dst_blocks must be 1-D of equal length")
-        rc = lib().pa_copy_blocks_scaled(
-            _dev(key_cache, "key_cache"), _dev(value_cache, "value_cache"),
-            _dev(k_scales, "k_scales"), _dev(v_scales, "v_scales"),
-            _dev(src_blocks, "src_blocks", torch.int32),
-            _dev(dst_blocks, "dst_blocks", torch.int32), src_blocks.shape[0], bs, hkv, d, nb,
-            _stream(stream))
-    _check(rc, "pa_copy_blocks_scaled")
+    rc = (_native or native()).copy_blocks_scaled(key_cache, value_cache, k_scales, v_scales,
+                                                  src_blocks, dst_blocks, stream)
+    if rc != PA_OK:
+        raise PAError(rc, "pa_copy_blocks_scaled")
 
 
 def pa_attention_scaled(q, key_cache, value_cache, k_scales, v_scales, block_table,
@@ -516,33 +449,12 @@ def pa_attention_scaled(q, key_cache, value_cache, k_scales, v_scales, block_tab
                         workspace=None, stream=None, shared_blocks=False):
     """``pa_attention`` over FP8 pools [NB, 16, Hkv, D] with scale bytes
     ``k_scales``/``v_scales`` uint8 [NB, Hkv]: q [T, Hq, D] -> out [T, Hq, D]."""
-    with torch.cuda.device(_on_device({
-            "q": q, "key_cache": key_cache, "value_cache": value_cache, "k_scales": k_scales,
-            "v_scales": v_scales, "block_table": block_table,
-            "query_start_loc": query_start_loc, "seq_lens": seq_lens, "out": out,
-            "workspace": workspace})):
-        nb, bs, hkv, d = _scaled_pools(key_cache, value_cache, k_scales, v_scales)
-        if q.dim() != 3 or q.shape[2] != d or out.shape != q.shape:
-            raise ValueError(f"q and out must both be [T, Hq, {d}]")
-        T, hq, _ = q.shape
-        dt = _DTYPES.get(q.dtype)
-        if dt is None or out.dtype != q.dtype:
-            raise TypeError("q and out must share a bf16/fp16 dtype")
-        R = _batch(block_table, query_start_loc, seq_lens, "query_start_loc", "seq_lens")
-        ws_ptr, ws_bytes = ctypes.c_void_p(0), 0
-        if workspace is not None and workspace.numel() > 0:
-            ws_ptr = _dev(workspace, "workspace")
-            ws_bytes = workspace.numel() * workspace.element_size()
-        rc = lib().pa_attention_scaled(
-            _dev(q, "q"), _dev(key_cache, "key_cache"), _dev(value_cache, "value_cache"),
-            _dev(k_scales, "k_scales"), _dev(v_scales, "v_scales"),
-            _dev(block_table, "block_table", torch.int32), block_table.shape[1],
-            _dev(query_start_loc, "query_start_loc", torch.int32),
-            _dev(seq_lens, "seq_lens", torch.int32), R, T, int(max_query_len), int(max_seq_len),
-            hq, hkv, d, bs, nb, float(scale), dt,
-            PA_ATTN_SHARED_BLOCKS if shared_blocks else 0, _dev(out, "out"), ws_ptr, ws_bytes,
-            _stream(stream))
-    _check(rc, "pa_attention_scaled")
+    rc = (_native or native()).attention_scaled(
+        q, key_cache, value_cache, k_scales, v_scales, block_table, query_start_loc, seq_lens,
+        max_query_len, max_seq_len, scale, out, workspace, stream,
+        PA_ATTN_SHARED_BLOCKS if shared_blocks else 0)
+    if rc != PA_OK:
+        raise PAError(rc, "pa_attention_scaled")
 
 
 NOALLOC_SCRATCH_BYTES = 32 << 20

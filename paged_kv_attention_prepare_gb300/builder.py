@@ -1,8 +1,9 @@
-"""Build ``libpa.so`` in-tree from ``csrc/*.cu`` with nvcc for sm_103a.
+"""Build ``libpa.so`` in-tree from ``csrc/*.cu`` with nvcc for sm_103a, and
+the Python binding's native half ``_native.so`` from ``csrc/binding.cpp``.
 
 Translation units compile in parallel; the link is a plain shared-library
-link (no relocatable device code).  Re-running is a no-op while the library
-is newer than every source and header.
+link (no relocatable device code).  Re-running is a no-op while the libraries
+are newer than every source and header.
 
     python -m paged_kv_attention_prepare_gb300.builder [--force] [--ptxas-info]
 """
@@ -15,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +24,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build", "pa")
 LIB = os.path.join(PKG, "libpa.so")
+BINDING = os.path.join(CSRC, "binding.cpp")
+NATIVE = os.path.join(PKG, "_native.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
@@ -37,17 +41,51 @@ def _nvcc() -> str:
 
 def _inputs():
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    deps = srcs + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [
+    deps = srcs + [BINDING] + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [
         os.path.join(ROOT, "include", "pa.h"), os.path.abspath(__file__)]
     return srcs, deps
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(NATIVE):
         return False
     _, deps = _inputs()
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
     return all(os.path.getmtime(d) <= t for d in deps)
+
+
+def _torch_dirs():
+    """torch's C++ header and library directories."""
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    return os.path.join(root, "include"), os.path.join(root, "lib")
+
+
+def _compile_binding() -> str:
+    include, _ = _torch_dirs()
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    obj = os.path.join(BUILD, "binding.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I" + os.path.join(ROOT, "include"),
+           "-isystem", include, "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(cuda, "include"), "-c", BINDING, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING}:\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    """Against libpa.so beside it, and torch's libraries (already loaded: the
+    package imports torch first)."""
+    _, libs = _torch_dirs()
+    tmp = NATIVE + f".{os.getpid()}.tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libpa.so", "-L" + libs,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN",
+           "-Wl,-rpath," + libs]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stderr}")
+    os.replace(tmp, NATIVE)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -66,8 +104,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(compile_one, srcs))
+        binding = binding.result()
     if verbose or ptxas_info:
         for obj, err in results:
             if err.strip():
@@ -78,6 +118,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 

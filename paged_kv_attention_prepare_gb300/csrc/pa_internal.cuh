@@ -98,6 +98,7 @@ struct CacheReadArgs {
     int32_t R, N, MB, NB, Hkv, bs;
     int32_t row;                         // elements per row (Hkv*D)
     int32_t head_shift;                  // block-scaled pools: log2(D / 8)
+    int32_t rows_per_warp;               // set by the launch
     void *key_out, *value_out;
     unsigned int *status;
 };

@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kScaledThreads, 4) cache_write_scaled_kernel(c
 // Read
 // ---------------------------------------------------------------------------
 
-constexpr int kReadRows = 8;    // rows a warp takes at a time
+constexpr int kReadRows = 8;    // rows a warp takes at a time, at most
 constexpr int kReadUnroll = 4;  // units of K and of V in flight per lane
 
 // kPool 0: 16-bit pools (a copy); 1: E4M3 pools with one scale each; 2: E4M3
@@ -226,10 +226,11 @@ __global__ void __launch_bounds__(kScaledThreads, 4) cache_read_kernel(const Cac
     if (blockIdx.x == 0 && threadIdx.x == 0 && (rows_in > a.N || rows_in < 0))
         flag(a.status, PA_CHECK_TOKEN_COUNT);
     const int rows_all = min(rows_in, a.N);
-    const long long step = (long long)gridDim.x * kScaledWarps * kReadRows;
-    for (long long t0 = ((long long)blockIdx.x * kScaledWarps + (threadIdx.x >> 5)) * kReadRows;
+    const int per = a.rows_per_warp;
+    const long long step = (long long)gridDim.x * kScaledWarps * per;
+    for (long long t0 = ((long long)blockIdx.x * kScaledWarps + (threadIdx.x >> 5)) * per;
          t0 < rows_all; t0 += step) {
-        const int rows = (int)min((long long)kReadRows, rows_all - t0);
+        const int rows = (int)min((long long)per, rows_all - t0);
         // The last request with row_starts[r] <= t0: 32 probes at a time.
         int lo = 0, n = R;                   // among requests lo .. lo + n - 1
         while (n > 1) {
@@ -378,8 +379,12 @@ pa_status launch_cache_read(CacheReadArgs a, int pool, pa_dtype dtype, cudaStrea
     if (a.N == 0 || a.R == 0) return PA_OK;
     a.status = status_word();
     if (!a.status) return PA_ERR_CUDA;
-    long long blocks = ((long long)a.N + kReadRows * kScaledWarps - 1) / (kReadRows * kScaledWarps);
+    // Few rows: fewer a warp, down to one, until they fill the GPU once.
     const long long cap = 4LL * num_sms();
+    a.rows_per_warp = kReadRows;
+    while (a.rows_per_warp > 1 && (long long)a.N < cap * kScaledWarps * a.rows_per_warp) a.rows_per_warp /= 2;
+    const int per_block = a.rows_per_warp * kScaledWarps;
+    long long blocks = ((long long)a.N + per_block - 1) / per_block;
     if (blocks > cap) blocks = cap;
     return dtype == PA_BF16 ? launch_read<__nv_bfloat16>(a, pool, (int)blocks, stream)
                             : launch_read<__half>(a, pool, (int)blocks, stream);
