@@ -86,6 +86,7 @@ struct Params {
     unsigned int *status;
     int launch_pdl;       // host side: the split-K grid as a programmatic dependent of the grid before
     int launch_part;      // host side: 0 split-K grid and merge pass, 1 the grid only, 2 the merge only
+    int max_tokens;       // host side: most query tokens of a request handled here (at least 1)
 };
 
 // Marker for an FP8 E4M3 cache element.
@@ -159,12 +160,20 @@ struct Cfg {
     // passes of kDC dims each: at 8 rows and head_dim 128 two passes keep the
     // buffer at the 4-row size, so three CTAs still fit an SM.
     static constexpr int kCombPasses = (RPI == 8 && D == 128) ? 2 : 1;
+    // Wide items (block-scaled pools): NT 8-row MMA tiles share a page's
+    // converted fragments, two CTAs per SM (their registers).
+    static constexpr int kNT = RPI > 8 ? RPI / 8 : 1;
+    static constexpr int kCtas = RPI > 8 && D == 128 ? 2 : kCtasPerSm;
+    // ... at head_dim 128 with q's fragments in shared memory (at two CTAs a
+    // thread has 168 registers; with q in them too 324 bytes spilled)
+    static constexpr bool kQShared = RPI > 8 && D == 128;
+    static_assert(RPI <= 8 || std::is_same<TC, Fp8Block>::value, "wide items: block-scaled pools only");
     static constexpr int kDC = D / kCombPasses;
     static constexpr int kComb = RPI * (kDC + 2);     // per warp: acc[row][kDC], m[row], l[row]
     static constexpr int kBytes = kStageBytes + kConsumerWarps * kComb * 4 +
                                   (2 * kStages + 2) * 8 + kCandidates * 8 + kQueue * 3 * 8 +
                                   (std::is_same<TC, Fp8Block>::value ? kStages / 2 * kSP * 4 : 0) +
-                                  1024;
+                                  (kQShared ? RPI * D * 2 + 16 : 0) + 1024;
 };
 
 // First stage of warp w's c-th (K, V) unit pair (the V unit takes the next
@@ -386,7 +395,7 @@ __device__ __forceinline__ int perm16(int k) { return ((0x27146350u >> (4 * (k &
 // kGroups: shared-partition group items (callers whose block tables may
 // share physical blocks); the kernel without them has no code for them.
 template <typename TQ, typename TC, int D, int RPI, bool kGroups>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, (Cfg<TC, D, RPI>::kCtas))
 paged_decode_kernel(const __grid_constant__ Params p) {
     using L = Lay<TC, D>;
     using TM = typename MmaIn<TQ, TC>::type;
@@ -410,6 +419,9 @@ paged_decode_kernel(const __grid_constant__ Params p) {
     // (K's low, V's next)
     constexpr bool kBlockScales = std::is_same<TC, Fp8Block>::value;
     uint32_t *unit_scales = reinterpret_cast<uint32_t *>(qitem + kQueue);
+    // wide items at head_dim 128: q's fragments, [tile][k-step pair][lane]
+    uint4 *q_frag = reinterpret_cast<uint4 *>(
+        (reinterpret_cast<uintptr_t>(unit_scales + (kBlockScales ? kSt / 2 * C::kSP : 0)) + 15) & ~uintptr_t(15));
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // arrivals that release a stage: group items need all four warps
@@ -525,12 +537,21 @@ paged_decode_kernel(const __grid_constant__ Params p) {
 
     if (warp == kConsumerWarps) {
         // =================== producer warp ===================
-        // Issue order: K unit 0, V unit 0, K unit 1, V unit 1, ... of each
-        // item, a unit being C::kSP consecutive pages of the request, unit j
-        // into the next stage pair of warp j mod 4.  A page is L::NSUB swizzled
-        // boxes of 16 rows (one per 128 bytes of a row), landing back to back.
+        // Units in order, K and V of each together: a unit is C::kSP
+        // consecutive pages of the request, unit j goes into the next stage
+        // pair of warp j mod 4.  A page is L::NSUB swizzled boxes of 16 rows
+        // (one per 128 bytes of a row), landing back to back.  Each copy of a
+        // unit (4 or 8 of them) is issued by a lane of its own, in one
+        // instruction of the warp: one lane issuing them in turn, with a wait
+        // and a shuffle around each, took 860-1100 cycles a unit and bound the
+        // FP8 layouts (256 requests of 2048 keys, 32/8, head_dim 64: 146 ->
+        // 129 us, head_dim 128: 209 -> 204 us).
         constexpr int kSP = C::kSP;
         constexpr int kPW = C::kPairsPerWarp;
+        constexpr int kCopies = kSP * L::NSUB;          // of K, and as many of V
+        const int copy_kv = lane >= kCopies ? 1 : 0;    // this lane's copy
+        const int copy_sp = (lane - copy_kv * kCopies) / L::NSUB;
+        const int copy_sub = (lane - copy_kv * kCopies) % L::NSUB;
         // pairs handed to each consumer warp so far, mod 256: one byte per warp
         uint32_t handed = 0;
         auto handed_to = [&](int w) { return (handed >> (8 * w)) & 0xffu; };
@@ -620,49 +641,32 @@ paged_decode_kernel(const __grid_constant__ Params p) {
                 const int n = min(32, npages - g0);
                 for (int pu = 0; ok && pu < n; pu += kSP) {
                     const int cnt = min(kSP, n - pu);   // pages in this unit
-                    int b[kSP];
-#pragma unroll
-                    for (int sp = 0; sp < kSP; ++sp) b[sp] = __shfl_sync(0xffffffffu, blk, min(pu + sp, 31));
                     const int w = ((g0 + pu) / kSP) % kConsumerWarps;
                     const uint32_t c = handed_to(w);
                     const uint32_t phase = (c / kPW) & 1u;
                     handed = (handed & ~(0xffu << (8 * w))) | (((c + 1) & 0xffu) << (8 * w));
-                    uint32_t us[kSP];
-                    if constexpr (kBlockScales) {
-#pragma unroll
-                        for (int sp = 0; sp < kSP; ++sp) us[sp] = __shfl_sync(0xffffffffu, sc, min(pu + sp, 31));
+                    const int stage = pair_stage<kPW>(w, c);   // K; V takes the next one
+                    const int page = __shfl_sync(0xffffffffu, blk, min(pu + copy_sp, 31));
+                    uint32_t us = 0;
+                    if constexpr (kBlockScales) us = __shfl_sync(0xffffffffu, sc, min(pu + lane, 31));
+                    bool freed = true;
+                    if (lane < 2) freed = mbar_wait(&empty[stage + lane], phase ^ 1);
+                    ok = __all_sync(0xffffffffu, freed);
+                    if (!ok) {
+                        if (lane == 0) flag(p.status, PA_CHECK_TIMEOUT);
+                        break;
                     }
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const int stage = pair_stage<kPW>(w, c) + kv;
-                        if (lane == 0) {
-                            if (!mbar_wait(&empty[stage], phase ^ 1)) {
-                                flag(p.status, PA_CHECK_TIMEOUT);
-                                ok = false;
-                            } else {
-                                // read by the consumers before they release K
-                                if constexpr (kBlockScales) {
-                                    if (kv == 0) {
-#pragma unroll
-                                        for (int sp = 0; sp < kSP; ++sp)
-                                            unit_scales[(stage >> 1) * kSP + sp] = us[sp];
-                                    }
-                                }
-                                mbar_arrive_expect_tx(&full[stage], cnt * L::kPageBytes);
-#pragma unroll
-                                for (int sp = 0; sp < kSP; ++sp) {
-                                    if (sp >= cnt) break;
-#pragma unroll
-                                    for (int sub = 0; sub < L::NSUB; ++sub)
-                                        tma_load_3d(stages + stage * C::kUnitBytes + sp * L::kPageBytes +
-                                                        sub * L::kSubBytes,
-                                                    kv ? &p.tmV : &p.tmK, &full[stage],
-                                                    sub * (L::SR / L::E), it.g, b[sp] * kPage);
-                                }
-                            }
-                        }
+                    if constexpr (kBlockScales) {   // read by the consumers before they release K
+                        if (lane < kSP) unit_scales[(stage >> 1) * kSP + lane] = us;
+                        __syncwarp();
                     }
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (lane < 2) mbar_arrive_expect_tx(&full[stage + lane], cnt * L::kPageBytes);
+                    __syncwarp();
+                    if (lane < 2 * kCopies && copy_sp < cnt)
+                        tma_load_3d(stages + (stage + copy_kv) * C::kUnitBytes + copy_sp * L::kPageBytes +
+                                        copy_sub * L::kSubBytes,
+                                    copy_kv ? &p.tmV : &p.tmK, &full[stage + copy_kv],
+                                    copy_sub * (L::SR / L::E), it.g, page * kPage);
                 }
             }
         }
@@ -731,6 +735,288 @@ paged_decode_kernel(const __grid_constant__ Params p) {
     // units every warp reads); without them a warp counts only its own.
     uint32_t handed = 0, taken = 0;
     uint32_t cpar = 0;
+
+    // ---- a wide item: NT tiles of 8 rows over every page of the warp's
+    //      units.  A page's K and V are read and widened once for all the
+    //      tiles, and the tiles' chains (scores, softmax, PV) are
+    //      independent, so one hides another's latency: with 8-row items a
+    //      request of many rows read its pages once per 8 rows, and a warp
+    //      issued an instruction every 9 cycles (64 requests of 1-8 tokens, 7
+    //      heads a group, head_dim 64: 53 us, 31% of the issue slots).  The
+    //      softmax is page by page here: a page's scores are NT * 4 registers.
+    constexpr int NT = C::kNT;
+    // The reference of a row that has seen no key: finite, so that no score
+    // needs a test for it (2^(-inf - kNoKey) is 0 too), and under every score.
+    constexpr float kNoKey = -1e38f;
+    auto wide_item = [&](const typename Walker<RPI>::Item &w, int k0, int k1, int npages, int qstart,
+                         int nrows, int pos0, int lim_all) -> bool {
+        constexpr int kSP = C::kSP;
+        const int row0 = w.chunk * RPI;
+        const int act = min(NT, (nrows - row0 + 7) / 8);   // tiles that hold rows
+        constexpr bool kQS = C::kQShared;
+        uint32_t qw[kQS ? 1 : NT][KS][2];
+        float ow[NT][KS][4];
+        float mw[NT][2], lw[NT][2];
+        int lim[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = row0 + 8 * t + 2 * tq + e;
+                lim[t][e] = r < nrows ? min(pos0 + r / p.G, k1 - 1) : -1;
+                mw[t][e] = kNoKey;
+                lw[t][e] = 0.f;
+            }
+#pragma unroll
+            for (int mt = 0; mt < KS; ++mt) ow[t][mt][0] = ow[t][mt][1] = ow[t][mt][2] = ow[t][mt][3] = 0.f;
+            const int rr = row0 + 8 * t + gq;
+            const bool have = rr < nrows;
+            const TQ *qrow = q + ((long long)(qstart + (have ? rr / p.G : 0)) * p.Hq + w.g * p.G +
+                                  (have ? rr % p.G : 0)) * D;
+#pragma unroll
+            for (int jj = 0; jj < NCH; ++jj) {
+                const int d0 = (tq + 4 * jj) * (16 / L::E);
+#pragma unroll
+                for (int h = 0; h < 16 / L::E / 8; ++h) {
+                    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+                    if (have) raw = *reinterpret_cast<const uint4 *>(qrow + d0 + 8 * h);
+                    const uint4 f = make_uint4(QConv<TQ, TM>::run(raw.x), QConv<TQ, TM>::run(raw.y),
+                                               QConv<TQ, TM>::run(raw.z), QConv<TQ, TM>::run(raw.w));
+                    const int s2 = jj * KPC + 2 * h;   // k-steps s2, s2 + 1
+                    if constexpr (kQS) {
+                        // every warp writes the same values, and no warp is
+                        // past the item before (its combine) here
+                        q_frag[(t * KS + s2) / 2 * 32 + lane] = f;
+                    } else {
+                        qw[t][s2][0] = f.x;
+                        qw[t][s2][1] = f.y;
+                        qw[t][s2 + 1][0] = f.z;
+                        qw[t][s2 + 1][1] = f.w;
+                    }
+                }
+            }
+        }
+        if constexpr (kQS) __syncwarp();
+        const int nunits = (npages + kSP - 1) / kSP;
+        uint32_t c = taken;
+        for (int pu = warp; pu < nunits; pu += kConsumerWarps, ++c) {
+            const int stK = pair_stage<C::kPairsPerWarp>(warp, c), stV = stK + 1;
+            const uint32_t ph = (c / C::kPairsPerWarp) & 1u;
+            if (!mbar_wait_warp(&full[stK], ph) || !mbar_wait_warp(&full[stV], ph)) {
+                flag(p.status, PA_CHECK_TIMEOUT);
+                return false;
+            }
+            const int cnt = min(kSP, npages - pu * kSP);
+#pragma unroll 1
+            for (int sp = 0; sp < cnt; ++sp) {
+                const int key0 = k0 + (pu * kSP + sp) * kPage;
+                const uint32_t sc = unit_scales[(stK >> 1) * kSP + sp];
+                // S^T of every tile
+                float sv[NT][4];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) sv[t][0] = sv[t][1] = sv[t][2] = sv[t][3] = 0.f;
+                const unsigned char *kpage = stages + stK * C::kUnitBytes + sp * L::kPageBytes;
+#pragma unroll
+                for (int jj = 0; jj < NCH; ++jj) {
+                    const uint4 ka = *reinterpret_cast<const uint4 *>(kpage + koff(koff_a, jj));
+                    const uint4 kb = *reinterpret_cast<const uint4 *>(kpage + koff(koff_b, jj));
+                    const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+                    for (int sub = 0; sub < KPC; sub += 2) {
+                        const int s2 = jj * KPC + sub;
+                        uint32_t a[2][4];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            e4m3x4_to_f16x4(wa[sub + x], a[x][0], a[x][2]);
+                            e4m3x4_to_f16x4(wb[sub + x], a[x][1], a[x][3]);
+                        }
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            if (t >= act) continue;
+                            uint4 f;
+                            if constexpr (kQS) f = q_frag[(t * KS + s2) / 2 * 32 + lane];
+                            else f = make_uint4(qw[t][s2][0], qw[t][s2][1], qw[t][s2 + 1][0], qw[t][s2 + 1][1]);
+                            Mma<TM>::run(sv[t], a[0][0], a[0][1], a[0][2], a[0][3], f.x, f.y);
+                            Mma<TM>::run(sv[t], a[1][0], a[1][1], a[1][2], a[1][3], f.z, f.w);
+                        }
+                    }
+                }
+                const float kf = qs * __uint_as_float((sc & 0xffu) << 23);
+                const float ev = (float)(int)((sc >> 8) - kScaleBias);
+                const float iv = __uint_as_float((254u - (sc >> 8)) << 23);
+                uint32_t hidden = 0;   // bit 4 t + e: score e of tile t is masked
+                if (key0 + kPage - 1 > lim_all) {
+                    const int pa = key0 + perm16(gq), pb = key0 + perm16(gq + 8);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            hidden |= ((e >> 1) ? pb : pa) > lim[t][e & 1] ? 1u << (4 * t + e) : 0u;
+                }
+                // x = t - m of each score, m the row's reference; the references
+                // move only when some row's x passes 8: one vote, not a
+                // reduction, on most pages.
+                float x[NT][4], top = -INFINITY;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if (t >= act) continue;
+                    const float b0 = ev - mw[t][0], b1 = ev - mw[t][1];
+                    x[t][0] = fmaf(sv[t][0], kf, b0);
+                    x[t][1] = fmaf(sv[t][1], kf, b1);
+                    x[t][2] = fmaf(sv[t][2], kf, b0);
+                    x[t][3] = fmaf(sv[t][3], kf, b1);
+                    if (hidden) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if ((hidden >> (4 * t + e)) & 1) x[t][e] = -INFINITY;
+                    }
+                    top = fmaxf(top, fmaxf(fmaxf(x[t][0], x[t][1]), fmaxf(x[t][2], x[t][3])));
+                }
+                if (__any_sync(0xffffffffu, top > 8.f)) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        if (t >= act) continue;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float t0 = fmaf(sv[t][e], kf, ev), t1 = fmaf(sv[t][e + 2], kf, ev);
+                            if ((hidden >> (4 * t + e)) & 1) t0 = -INFINITY;
+                            if ((hidden >> (4 * t + e + 2)) & 1) t1 = -INFINITY;
+                            float mx = fmaxf(t0, t1);
+#pragma unroll
+                            for (int y = 4; y < 32; y <<= 1)
+                                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
+                            if (mx > mw[t][e] + 8.f) {
+                                const float al = fast_exp2(mw[t][e] - mx);
+                                mw[t][e] = mx;
+                                lw[t][e] *= al;
+#pragma unroll
+                                for (int mt = 0; mt < KS; ++mt) {
+                                    ow[t][mt][e] *= al;
+                                    ow[t][mt][e + 2] *= al;
+                                }
+                                x[t][e] = t0 - mx;
+                                x[t][e + 2] = t1 - mx;
+                            }
+                        }
+                    }
+                }
+                uint32_t pf[NT][2];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if (t >= act) continue;
+                    float pv[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) pv[e] = fast_exp2(x[t][e]);
+                    lw[t][0] = fmaf(pv[0] + pv[2], iv, lw[t][0]);
+                    lw[t][1] = fmaf(pv[1] + pv[3], iv, lw[t][1]);
+                    pf[t][0] = movmatrix_trans(Mma<TM>::pack(pv[0], pv[1]));
+                    pf[t][1] = movmatrix_trans(Mma<TM>::pack(pv[2], pv[3]));
+                }
+                // O^T += V^T P^T of every tile; slots past the context are zeroed
+                const int nvalid = min(kPage, k1 - key0);
+                const unsigned char *vpage = stages + stV * C::kUnitBytes + sp * L::kPageBytes;
+                constexpr int NW = D / 32;
+                uint32_t vw[4][NW];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (NW == 4) {
+                        const uint4 v4 = *reinterpret_cast<const uint4 *>(vpage + voff[e]);
+                        vw[e][0] = v4.x;
+                        vw[e][1] = v4.y;
+                        vw[e][2] = v4.z;
+                        vw[e][3] = v4.w;
+                    } else {
+                        const uint2 v2 = *reinterpret_cast<const uint2 *>(vpage + voff[e]);
+                        vw[e][0] = v2.x;
+                        vw[e][1] = v2.y;
+                    }
+                    if (nvalid < kPage && vkey(e) >= nvalid) {
+#pragma unroll
+                        for (int tp = 0; tp < NW; ++tp) vw[e][tp] = 0u;
+                    }
+                }
+#pragma unroll
+                for (int tp = 0; tp < NW; ++tp) {
+                    uint32_t a0, a1, a2, a3, c0, c1, c2, c3;
+                    e4m3x4_to_f16x4(__byte_perm(vw[0][tp], vw[1][tp], 0x5140), a0, a1);
+                    e4m3x4_to_f16x4(__byte_perm(vw[2][tp], vw[3][tp], 0x5140), a2, a3);
+                    e4m3x4_to_f16x4(__byte_perm(vw[0][tp], vw[1][tp], 0x7362), c0, c1);
+                    e4m3x4_to_f16x4(__byte_perm(vw[2][tp], vw[3][tp], 0x7362), c2, c3);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        if (t >= act) continue;
+                        Mma<TM>::run(ow[t][2 * tp], a0, a1, a2, a3, pf[t][0], pf[t][1]);
+                        Mma<TM>::run(ow[t][2 * tp + 1], c0, c1, c2, c3, pf[t][0], pf[t][1]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&empty[stK]);
+                mbar_arrive(&empty[stV]);
+            }
+        }
+        taken = c;
+        // The four warps' states through shared memory, then out (as below).
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if (t >= act) continue;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) lw[t][e] += __shfl_xor_sync(0xffffffffu, lw[t][e], x);
+                const int r = 8 * t + 2 * tq + e;
+#pragma unroll
+                for (int mt = 0; mt < KS; ++mt) {
+                    const int d = gq * (D / 8) + 4 * (mt >> 1) + 2 * (mt & 1);
+                    *reinterpret_cast<float2 *>(cw + r * D + d) = make_float2(ow[t][mt][e], ow[t][mt][e + 2]);
+                }
+                if (gq == 0) {
+                    cw[RPI * D + r] = mw[t][e];
+                    cw[RPI * D + RPI + r] = lw[t][e];
+                }
+            }
+        }
+        if (!consumer_sync(cbar, cpar, lane)) {
+            flag(p.status, PA_CHECK_TIMEOUT);
+            return false;
+        }
+        const int rows = min(8 * act, nrows - row0);
+        for (int o2 = tid; o2 < rows * (D / 2); o2 += kConsumers) {
+            const int r = o2 / (D / 2), d = (o2 % (D / 2)) * 2;
+            float M = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < kConsumerWarps; ++x) M = fmaxf(M, comb[x * C::kComb + RPI * D + r]);
+            float Ls = 0.f, s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int x = 0; x < kConsumerWarps; ++x) {
+                const float *cx = comb + x * C::kComb;
+                const float mx = cx[RPI * D + r];
+                const float sx = fast_exp2(mx - M);
+                Ls += sx * cx[RPI * D + RPI + r];
+                const float2 v = *reinterpret_cast<const float2 *>(cx + r * D + d);
+                s0 += sx * v.x;
+                s1 += sx * v.y;
+            }
+            if (w.pslot < 0) {
+                const float inv = 1.f / Ls;
+                const int rr = row0 + r;
+                TQ *dst = reinterpret_cast<TQ *>(p.out) +
+                          ((long long)(qstart + rr / p.G) * p.Hq + w.g * p.G + rr % p.G) * D + d;
+                *reinterpret_cast<uint32_t *>(dst) = Elt<TQ>::pack2(s0 * inv, s1 * inv);
+            } else {
+                *reinterpret_cast<float2 *>(p.part_o + (w.pslot * RPI + r) * D + d) = make_float2(s0, s1);
+                if (d == 0)
+                    *reinterpret_cast<float2 *>(p.part_ml + (w.pslot * RPI + r) * 2) = make_float2(M, Ls);
+            }
+        }
+        if (!consumer_sync(cbar, cpar, lane)) {   // the combine buffer is free again
+            flag(p.status, PA_CHECK_TIMEOUT);
+            return false;
+        }
+        return true;
+    };
+
     bool ok = true;
     for (long long k = 0; ok; ++k) {
         long long i = blockIdx.x + k * gridDim.x;
@@ -773,6 +1059,14 @@ paged_decode_kernel(const __grid_constant__ Params p) {
         // Pages whose last key every row of the item sees need no mask (rows
         // past the item then pick up scores, but they are never written out).
         const int lim_all = grp ? k1 - 1 : min(pos0 + (it.chunk * RPI) / p.G, k1 - 1);
+
+        if constexpr (RPI > 8) {
+            if (!wide_item(it, k0, k1, npages, qstart, nrows, pos0, lim_all)) {
+                ok = false;
+                break;
+            }
+            continue;
+        }
 
         // Q^T fragments (B operand): row gq of the item (of the warp's rows
         // for a group), this lane's dims.
@@ -905,13 +1199,15 @@ paged_decode_kernel(const __grid_constant__ Params p) {
                 mx0 = fmaxf(mx0, fmaxf(sv[sp][0], sv[sp][2]));
                 mx1 = fmaxf(mx1, fmaxf(sv[sp][1], sv[sp][3]));
             }
+            // (one vote on most units: a row's maximum is only reduced over its
+            // lanes when some lane's passes its reference)
+            if (__any_sync(0xffffffffu, mx0 > m0 + 8.f || mx1 > m1 + 8.f)) {
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) {
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, x));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, x));
-            }
-            const bool up0 = mx0 > m0 + 8.f, up1 = mx1 > m1 + 8.f;
-            if (up0 || up1) {
+                for (int x = 4; x < 32; x <<= 1) {
+                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, x));
+                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, x));
+                }
+                const bool up0 = mx0 > m0 + 8.f, up1 = mx1 > m1 + 8.f;
                 const float al0 = up0 ? fast_exp2(m0 - mx0) : 1.f;
                 const float al1 = up1 ? fast_exp2(m1 - mx1) : 1.f;
                 if (up0) m0 = mx0;
@@ -1272,7 +1568,7 @@ static __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const __
     const int g = h / p.G;
     const int cnt_w = nsplit > sub ? (nsplit - sub + WPH - 1) / WPH : 0;   // this warp's partitions
     const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml);
-    for (int tl = 0; tl < n; ++tl) {
+    for (int tl = blockIdx.y; tl < n; tl += gridDim.y) {
         const int rr = tl * p.G + h % p.G;
         const int chunk = rr / RPI, j = rr % RPI;
         const long long first = pbase + ((long long)g * nchunks + chunk) * nsplit;
@@ -1371,7 +1667,11 @@ static pa_status launch_merge(const Params &prm, cudaStream_t stream) {
     constexpr int kHeads = kMergeWarps / WPH;
     const long long groups = (prm.Hq + kHeads - 1) / kHeads;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(prm.R * groups));
+    // A CTA per query token too, as far as two waves of CTAs go (a CTA takes
+    // every gridDim.y-th token of its request).
+    long long tokens = prm.R * groups > 0 ? 16LL * num_sms() / (prm.R * groups) : 1;
+    tokens = tokens < 1 ? 1 : tokens > prm.max_tokens ? prm.max_tokens : tokens;
+    cfg.gridDim = dim3((unsigned)(prm.R * groups), (unsigned)tokens);
     cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -1434,7 +1734,9 @@ template <typename TQ, typename TC, int D, int RPI>
 pa_status launch_typed(Params &prm, long long max_items, long long merge_splits, bool groups,
                        cudaStream_t stream) {
     if (prm.launch_part != 2) {
-        const pa_status st = groups ? launch_split_k<TQ, TC, D, RPI, true>(prm, max_items, stream)
+        pa_status st;
+        if constexpr (RPI > 8) st = launch_split_k<TQ, TC, D, RPI, false>(prm, max_items, stream);
+        else st = groups ? launch_split_k<TQ, TC, D, RPI, true>(prm, max_items, stream)
                                     : launch_split_k<TQ, TC, D, RPI, false>(prm, max_items, stream);
         if (st != PA_OK) return st;
     }
@@ -1451,9 +1753,14 @@ pa_status launch_typed(Params &prm, long long max_items, long long merge_splits,
     return PA_OK;
 }
 
+// Rows of a wide item: as many 8-row tiles as two CTAs' registers hold.
+constexpr int wide_rows(int D) { return 16; }
+
 template <typename TQ, typename TC, int D>
 pa_status dispatch_rpi(int rpi, Params &prm, long long grid, long long merge, bool groups,
                        cudaStream_t stream) {
+    if constexpr (std::is_same<TC, Fp8Block>::value)
+        if (rpi > 8) return launch_typed<TQ, TC, D, wide_rows(D)>(prm, grid, merge, false, stream);
     switch (rpi) {
         case 1: return launch_typed<TQ, TC, D, 1>(prm, grid, merge, groups, stream);
         case 2: return launch_typed<TQ, TC, D, 2>(prm, grid, merge, groups, stream);
@@ -1582,8 +1889,13 @@ pa_status launch_decode(const AttnArgs &a, int tau, cudaStream_t stream) {
     if (!prm.status) return PA_ERR_CUDA;
     prm.launch_pdl = a.pdl ? 1 : 0;
     prm.launch_part = a.decode_part;
+    const int max_n = a.max_q < tau ? a.max_q : tau;
+    prm.max_tokens = max_n < 1 ? 1 : max_n > 64 ? 64 : max_n;
     prm.item_counter = a.ctrl ? a.ctrl + kCtrlDecodeCounter : nullptr;
-    const int rpi = rows_per_item(prm.G, a.max_q < tau ? a.max_q : tau);
+    // Block-scaled pools, no request for the tensor-core kernel, and requests
+    // of more than 8 rows on average: wide items.
+    const bool wide = a.k_bscales && a.max_q <= tau && (long long)a.T * prm.G > 8LL * a.R;
+    const int rpi = wide ? wide_rows(a.D) : rows_per_item(prm.G, a.max_q < tau ? a.max_q : tau);
 
     // Workspace: per-request metadata, then (m, l) and o partials.
     const size_t meta = round_up((size_t)a.R * 16);
@@ -1628,7 +1940,7 @@ pa_status launch_decode(const AttnArgs &a, int tau, cudaStream_t stream) {
     // the merge pass (when partitions exist) sizes itself by the most partitions a request can have
     const long long merge_splits = merge ? splits : 0;
     // group items need the partial slots (a merge pass) and the item queue
-    const bool groups = (a.flags & PA_ATTN_SHARED_BLOCKS) && merge && a.ctrl;
+    const bool groups = (a.flags & PA_ATTN_SHARED_BLOCKS) && merge && a.ctrl && !wide;
     if (a.k_bscales)
         return a.dtype == PA_BF16
                    ? dispatch_scaled<__nv_bfloat16>(a.D, rpi, prm, grid, merge_splits, groups, stream)

@@ -48,8 +48,14 @@
 // multiply-add as the softmax scale, and its V exponent ev in the addend: the
 // weights w = 2^(s + ev - m), m the running max of s + ev, carry V's scale
 // into PV, and the row sum takes a page's weights times 2^-ev.  The producer
-// leaves the three numbers of each page in shared memory, one copy per V
-// stage.
+// leaves these numbers for each page in shared memory, one copy per V stage.
+// 5000-token chunk at 2048, 32/8, head_dim 128: 377 us against 323 with one
+// scale per pool; the softmax warps' issue slots are the price (they share two
+// quarters of the SM with the widening warps, and 12 more instructions a page
+// are 15% of theirs).  Measured and not kept: bringing a tile's pages to one
+// exponent while widening (an f16 multiply per pair there: 382 us), four
+// widening warps (registers capped at 128: 396 us), landing buffers apart from
+// the f16 stages (389 us).
 #include <cudaTypedefs.h>
 
 #include <climits>
@@ -84,6 +90,9 @@ struct Conv {
 constexpr uint32_t kBf16F16Max = 0x477Fu;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.f;  // log2 units
+// Block-scaled pools: V's exponents spread the weights further, so the reference
+// moves later; P stays below 2^14, inside f16.
+constexpr float kRescaleThresholdBS = 14.f;
 constexpr int kTauDefault = 16;           // longer query chunks take this kernel
 
 struct Params {
@@ -130,7 +139,7 @@ struct Cfg {
     // block-scaled pools: each page's (K factor, V exponent, 2^-ev), per V
     // stage, right after the control block (in the staging area's alignment
     // gap at head_dim 64)
-    static constexpr int kScaleBytes = 2 * kPagesPerTile * 16;
+    static constexpr int kScaleBytes = 2 * kPagesPerTile * (16 + 8);
     // TMEM columns: S_A 0, O_A 128, S_B 256, O_B 384
     __device__ static constexpr uint32_t col_s(int slot) { return (uint32_t)slot * 256; }
     __device__ static constexpr uint32_t col_o(int slot) { return (uint32_t)slot * 256 + 128; }
@@ -592,8 +601,10 @@ paged_prefill_kernel(const __grid_constant__ Params p) {
     volatile int *v_src = split_fmt + 2;        // [3]
     static_assert(B_COUNT * 8 + (2 + kQueue + 2 * 3 + 2 + 3) * 4 <= 512, "control block");
     static_assert(!BS || F8, "block scales belong to FP8 pools");
-    // block-scaled pools: [2 V stages][pages of a tile] (K factor, V exponent, 2^-ev)
+    // block-scaled pools: [2 V stages][pages of a tile], K factor and V
+    // exponent, then 2^-ev, each twice (the operands of packed arithmetic)
     float4 *page_scales = reinterpret_cast<float4 *>(reinterpret_cast<unsigned char *>(bar) + 512);
+    float2 *page_iv = reinterpret_cast<float2 *>(page_scales + 2 * kPagesPerTile);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // A grid launched after this one as a programmatic dependent (the
@@ -781,8 +792,10 @@ paged_prefill_kernel(const __grid_constant__ Params p) {
                             if (lane < kPagesPerTile) {
                                 const int ek = clamp_scale((int)kb) - kScaleBias;
                                 const int ev = clamp_scale((int)vb) - kScaleBias;
+                                const float kf = p.qscale * pow2f(ek);
                                 page_scales[st * kPagesPerTile + lane] =
-                                    make_float4(p.qscale * pow2f(ek), (float)ev, pow2f(-ev), 0.f);
+                                    make_float4(kf, kf, (float)ev, (float)ev);
+                                page_iv[st * kPagesPerTile + lane] = make_float2(pow2f(-ev), pow2f(-ev));
                             }
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&bar[B_PSCALE + st]);
@@ -1099,7 +1112,7 @@ paged_prefill_kernel(const __grid_constant__ Params p) {
                 tc_fence_after();
                 const int key0 = j * kBN;
                 const bool full_tile = key0 + kBN - 1 <= pos;
-                if constexpr (!F8) {
+                if constexpr (!F8 || (BS && D == 64)) {
                     // One TMEM pass, 64 columns at a time: the half's row max (scale
                     // > 0 keeps the argmax), then P = exp2(s*c - m_ref) in packed
                     // f16 pairs written over the scores already read (64 keys ->
@@ -1110,7 +1123,12 @@ paged_prefill_kernel(const __grid_constant__ Params p) {
                     // TMEM (rare: only when the second half moves it again), the
                     // tile's partial sum, and O and l of earlier tiles once per
                     // tile.  A row with no visible key is never written out, so
-                    // any NaN stays in its own row.
+                    // any NaN stays in its own row.  Block-scaled pools: the same,
+                    // with the factor, exponent and sum of each page's 16 columns
+                    // its own.
+                    const int sst = BS ? (int)((t0 + j) & 1) : 0;
+                    const float4 *ps = page_scales + sst * kPagesPerTile;
+                    const float2 *pv = page_iv + sst * kPagesPerTile;
                     const float m_prev = m_ref;
                     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     #pragma unroll
@@ -1118,19 +1136,41 @@ paged_prefill_kernel(const __grid_constant__ Params p) {
                         uint32_t r[64];
                         tmem_ld32(colS + hh * 64, *reinterpret_cast<uint32_t (*)[32]>(r));
                         tmem_ld32(colS + hh * 64 + 32, *reinterpret_cast<uint32_t (*)[32]>(r + 32));
+                        // the tile's scales, while the scores come
+                        float4 sc[BS ? 4 : 1];
+                        float2 iv[BS ? 4 : 1];
+                        if constexpr (BS) {
+                            if (hh == 0 &&
+                                !mbar_wait_warp(&bar[B_PSCALE + sst], (uint32_t)(((t0 + j) >> 1) & 1)))
+                                ok = false;   // the scales are then stale: the item is given up below
+    #pragma unroll
+                            for (int pg = 0; pg < 4; ++pg) {
+                                sc[pg] = ps[hh * 4 + pg];
+                                iv[pg] = pv[hh * 4 + pg];
+                            }
+                        }
                         tmem_wait_ld();
                         if (!full_tile) {
     #pragma unroll
                             for (int k = 0; k < 64; ++k)
                                 if (key0 + hh * 64 + k > pos) r[k] = 0xff800000u;
                         }
+                        // four chains: of every fourth pair, or (block scales) of a page
                         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        auto chain = [](int k) { return BS ? k >> 4 : (k >> 1) & 3; };
     #pragma unroll
                         for (int k = 0; k < 64; k += 2)
-                            m4[(k >> 1) & 3] = fmaxf(m4[(k >> 1) & 3],
-                                                     fmaxf(__uint_as_float(r[k]), __uint_as_float(r[k + 1])));
-                        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2.x;
-                        const bool need = mx > m_ref + kRescaleThreshold;
+                            m4[chain(k)] = fmaxf(m4[chain(k)],
+                                                 fmaxf(__uint_as_float(r[k]), __uint_as_float(r[k + 1])));
+                        float mx;
+                        if constexpr (BS) {
+    #pragma unroll
+                            for (int pg = 0; pg < 4; ++pg) m4[pg] = fmaf(m4[pg], sc[pg].x, sc[pg].z);
+                            mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                        } else {
+                            mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2.x;
+                        }
+                        const bool need = mx > m_ref + (BS ? kRescaleThresholdBS : kRescaleThreshold);
                         if (need) {
                             const float alpha = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - mx);
                             acc[0].x *= alpha;
@@ -1155,19 +1195,40 @@ paged_prefill_kernel(const __grid_constant__ Params p) {
                             tmem_st32(colS, w);
                         }
                         if (need) m_ref = mx;
-                        const float2 mneg = make_float2(-m_ref, -m_ref);
                         uint32_t w[32];
+                        if constexpr (BS) {
     #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            float2 y = __ffma2_rn(make_float2(__uint_as_float(r[2 * e]),
-                                                              __uint_as_float(r[2 * e + 1])), c2, mneg);
-                            y.x = fast_exp2(y.x);
-                            y.y = fast_exp2(y.y);
-                            acc[e & 1] = __fadd2_rn(acc[e & 1], y);
-                            w[e] = Elt<__half>::pack2(y.x, y.y);
+                            for (int pg = 0; pg < 4; ++pg) {
+                                const float2 kf = make_float2(sc[pg].x, sc[pg].y);
+                                const float2 add = __fadd2_rn(make_float2(sc[pg].z, sc[pg].w),
+                                                              make_float2(-m_ref, -m_ref));
+                                float2 sum;
+    #pragma unroll
+                                for (int e = 8 * pg; e < 8 * pg + 8; ++e) {
+                                    float2 y = __ffma2_rn(make_float2(__uint_as_float(r[2 * e]),
+                                                                      __uint_as_float(r[2 * e + 1])), kf, add);
+                                    y.x = fast_exp2(y.x);
+                                    y.y = fast_exp2(y.y);
+                                    sum = e == 8 * pg ? y : __fadd2_rn(sum, y);
+                                    w[e] = Elt<__half>::pack2(y.x, y.y);
+                                }
+                                acc[pg & 1] = __ffma2_rn(sum, iv[pg], acc[pg & 1]);
+                            }
+                        } else {
+                            const float2 mneg = make_float2(-m_ref, -m_ref);
+    #pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                float2 y = __ffma2_rn(make_float2(__uint_as_float(r[2 * e]),
+                                                                  __uint_as_float(r[2 * e + 1])), c2, mneg);
+                                y.x = fast_exp2(y.x);
+                                y.y = fast_exp2(y.y);
+                                acc[e & 1] = __fadd2_rn(acc[e & 1], y);
+                                w[e] = Elt<__half>::pack2(y.x, y.y);
+                            }
                         }
                         tmem_st32(colS + hh * 64, w);
                     }
+                    if (BS && !ok) break;
                     if (j > 0 && __any_sync(0xffffffffu, m_ref != m_prev)) {
                         // O holds PV of tiles < j, all complete: S_j's commit (waited
                         // above) covers every MMA issued before it.  Rescale.
@@ -1185,114 +1246,61 @@ paged_prefill_kernel(const __grid_constant__ Params p) {
                     }
                     tmem_wait_st();
                     l += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-                } else if constexpr (BS) {
-                    // Block-scaled pools: the two passes below, page by page.
-                    const int sst = (int)((t0 + j) & 1);
-                    if (!mbar_wait_warp(&bar[B_PSCALE + sst], (uint32_t)(((t0 + j) >> 1) & 1))) {
-                        ok = false;
-                        break;
-                    }
+                } else {
+                    // FP8 pools: two passes over the scores (row max, then P).
+                    // The one-pass form above measured slower here when scores
+                    // spread widely (427 against 378 us on the mixed step's
+                    // chunk over unscaled pools).  Block-scaled pools: two
+                    // passes at head_dim 128 (one: 397 against 377 us on the
+                    // 5000-token chunk), one at 64 (five prompts of up to 1300
+                    // tokens, 16/16 heads: 41.5 -> 39.0 us).
+                    // Pass 1: row max of the raw scores (scale > 0 keeps the
+                    // argmax), 64 columns per TMEM round trip, four chains (of
+                    // every fourth pair; block scales: of a page).
+                    const int sst = BS ? (int)((t0 + j) & 1) : 0;
                     const float4 *ps = page_scales + sst * kPagesPerTile;
+                    const float2 *pv = page_iv + sst * kPagesPerTile;
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     float mx = -INFINITY;
     #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
                         uint32_t r[64];
                         tmem_ld32(colS + hh * 64, *reinterpret_cast<uint32_t (*)[32]>(r));
                         tmem_ld32(colS + hh * 64 + 32, *reinterpret_cast<uint32_t (*)[32]>(r + 32));
+                        if constexpr (BS) {
+                            // the tile's scales, while the scores come
+                            if (hh == 0 &&
+                                !mbar_wait_warp(&bar[B_PSCALE + sst], (uint32_t)(((t0 + j) >> 1) & 1)))
+                                ok = false;   // they are then stale: the item is given up below
+                        }
                         tmem_wait_ld();
                         if (!full_tile) {
     #pragma unroll
                             for (int k = 0; k < 64; ++k)
                                 if (key0 + hh * 64 + k > pos) r[k] = 0xff800000u;
                         }
+                        if constexpr (BS) {
     #pragma unroll
-                        for (int pg = 0; pg < 4; ++pg) {
-                            const float4 sc = ps[hh * 4 + pg];
-                            float m2[2] = {-INFINITY, -INFINITY};
+                            for (int pg = 0; pg < 4; ++pg) {
+                                const float4 sc = ps[hh * 4 + pg];
+                                float m2 = -INFINITY;
     #pragma unroll
-                            for (int k = 0; k < 16; k += 2)
-                                m2[(k >> 1) & 1] =
-                                    fmaxf(m2[(k >> 1) & 1], fmaxf(__uint_as_float(r[16 * pg + k]),
-                                                                  __uint_as_float(r[16 * pg + k + 1])));
-                            mx = fmaxf(mx, fmaf(fmaxf(m2[0], m2[1]), sc.x, sc.y));
-                        }
-                    }
-                    const bool need = mx > m_ref + kRescaleThreshold;
-                    if (j > 0 && __any_sync(0xffffffffu, need)) {
-                        // O holds PV of tiles < j, all complete: S_j's commit (waited
-                        // above) covers every MMA issued before it.  Rescale.
-                        const float alpha = need ? fast_exp2(m_ref - mx) : 1.f;
-    #pragma unroll
-                        for (int cc = 0; cc < D; cc += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(colO + cc, o);
-                            tmem_wait_ld();
-    #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st32(colO + cc, o);
-                        }
-                        tmem_wait_st();
-                        if (need) l *= alpha;
-                    }
-                    if (need) m_ref = mx;
-    #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        uint32_t r[64];
-                        tmem_ld32(colS + hh * 64, *reinterpret_cast<uint32_t (*)[32]>(r));
-                        tmem_ld32(colS + hh * 64 + 32, *reinterpret_cast<uint32_t (*)[32]>(r + 32));
-                        tmem_wait_ld();
-                        if (!full_tile) {
-    #pragma unroll
-                            for (int k = 0; k < 64; ++k)
-                                if (key0 + hh * 64 + k > pos) r[k] = 0xff800000u;
-                        }
-                        uint32_t w[32];
-    #pragma unroll
-                        for (int pg = 0; pg < 4; ++pg) {
-                            const float4 sc = ps[hh * 4 + pg];
-                            const float2 kf = make_float2(sc.x, sc.x);
-                            const float2 add = make_float2(sc.y - m_ref, sc.y - m_ref);
-                            float2 acc = make_float2(0.f, 0.f);
-    #pragma unroll
-                            for (int e = 8 * pg; e < 8 * pg + 8; ++e) {
-                                float2 y = __ffma2_rn(make_float2(__uint_as_float(r[2 * e]),
-                                                                  __uint_as_float(r[2 * e + 1])), kf, add);
-                                y.x = fast_exp2(y.x);
-                                y.y = fast_exp2(y.y);
-                                acc = __fadd2_rn(acc, y);
-                                w[e] = Elt<__half>::pack2(y.x, y.y);
+                                for (int k = 16 * pg; k < 16 * pg + 16; k += 2)
+                                    m2 = fmaxf(m2, fmaxf(__uint_as_float(r[k]), __uint_as_float(r[k + 1])));
+                                m4[pg] = fmaxf(m4[pg], fmaf(m2, sc.x, sc.z));
                             }
-                            l = fmaf(acc.x + acc.y, sc.z, l);
+                        } else {
+    #pragma unroll
+                            for (int k = 0; k < 64; k += 2)
+                                m4[(k >> 1) & 3] =
+                                    fmaxf(m4[(k >> 1) & 3],
+                                          fmaxf(__uint_as_float(r[k]), __uint_as_float(r[k + 1])));
                         }
-                        tmem_st32(colS + hh * 64, w);
                     }
-                    tmem_wait_st();
-                } else {
-                    // FP8 pools: two passes over the scores (row max, then P).
-                    // The one-pass form above measured slower here when scores
-                    // spread widely (427 against 378 us on the mixed step's
-                    // chunk over unscaled pools).
-                    // Pass 1: row max of the raw scores (scale > 0 keeps the
-                    // argmax), 64 columns per TMEM round trip, four chains.
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        uint32_t r[64];
-                        tmem_ld32(colS + hh * 64, *reinterpret_cast<uint32_t (*)[32]>(r));
-                        tmem_ld32(colS + hh * 64 + 32, *reinterpret_cast<uint32_t (*)[32]>(r + 32));
-                        tmem_wait_ld();
-                        if (!full_tile) {
-    #pragma unroll
-                            for (int k = 0; k < 64; ++k)
-                                if (key0 + hh * 64 + k > pos) r[k] = 0xff800000u;
-                        }
-    #pragma unroll
-                        for (int k = 0; k < 64; k += 2)
-                            m4[(k >> 1) & 3] = fmaxf(m4[(k >> 1) & 3],
-                                                     fmaxf(__uint_as_float(r[k]), __uint_as_float(r[k + 1])));
-                    }
-                    const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2.x;
-                    const bool need = mx > m_ref + kRescaleThreshold;
+                    mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    if constexpr (!BS) mx *= c2.x;
+                    if (BS && !ok) break;
+                    const bool need = mx > m_ref + (BS ? kRescaleThresholdBS : kRescaleThreshold);
                     if (j > 0 && __any_sync(0xffffffffu, need)) {
                         // O holds PV of tiles < j, all complete: S_j's commit (waited
                         // above) covers every MMA issued before it.  Rescale.
@@ -1328,14 +1336,34 @@ paged_prefill_kernel(const __grid_constant__ Params p) {
                                 if (key0 + hh * 64 + k > pos) r[k] = 0xff800000u;
                         }
                         uint32_t w[32];
+                        if constexpr (BS) {
     #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            float2 y = __ffma2_rn(make_float2(__uint_as_float(r[2 * e]),
-                                                              __uint_as_float(r[2 * e + 1])), c2, mneg);
-                            y.x = fast_exp2(y.x);
-                            y.y = fast_exp2(y.y);
-                            acc[e & 1] = __fadd2_rn(acc[e & 1], y);
-                            w[e] = Elt<__half>::pack2(y.x, y.y);
+                            for (int pg = 0; pg < 4; ++pg) {
+                                const float4 sc = ps[hh * 4 + pg];
+                                const float2 kf = make_float2(sc.x, sc.y);
+                                const float2 add = __fadd2_rn(make_float2(sc.z, sc.w), mneg);
+                                float2 sum;
+    #pragma unroll
+                                for (int e = 8 * pg; e < 8 * pg + 8; ++e) {
+                                    float2 y = __ffma2_rn(make_float2(__uint_as_float(r[2 * e]),
+                                                                      __uint_as_float(r[2 * e + 1])), kf, add);
+                                    y.x = fast_exp2(y.x);
+                                    y.y = fast_exp2(y.y);
+                                    sum = e == 8 * pg ? y : __fadd2_rn(sum, y);
+                                    w[e] = Elt<__half>::pack2(y.x, y.y);
+                                }
+                                acc[pg & 1] = __ffma2_rn(sum, pv[hh * 4 + pg], acc[pg & 1]);
+                            }
+                        } else {
+    #pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                float2 y = __ffma2_rn(make_float2(__uint_as_float(r[2 * e]),
+                                                                  __uint_as_float(r[2 * e + 1])), c2, mneg);
+                                y.x = fast_exp2(y.x);
+                                y.y = fast_exp2(y.y);
+                                acc[e & 1] = __fadd2_rn(acc[e & 1], y);
+                                w[e] = Elt<__half>::pack2(y.x, y.y);
+                            }
                         }
                         tmem_st32(colS + hh * 64, w);
                     }
