@@ -107,6 +107,7 @@ struct Params {
     int R, T, MB, NB, Hq, Hkv, G;
     int TT;         // query tokens per 128-row tile: floor(128 / G)
     int tau;        // requests with more than tau query tokens are handled here
+    int max_seq;    // tau 0 (no other kernel checks the lengths): the caller's bound on seq_lens
     float qscale;   // softmax scale * log2(e)
     const float *k_scale, *v_scale;   // FP8 pools (device scalars; NULL = 1)
     const uint8_t *k_bscales, *v_bscales;   // block-scaled FP8 pools: [NB][Hkv] scale bytes
@@ -318,8 +319,12 @@ struct Walker {
             const int b = p->qsl[r + 1];
             n = b - a;
             L = p->seq_lens[r];
-            const bool sane = a >= 0 && b <= p->T && n >= 0 && L >= n &&
-                              (L + kPage - 1) / kPage <= p->MB;
+            bool sane = a >= 0 && b <= p->T && n >= 0 && L >= n &&
+                        (L + kPage - 1) / kPage <= p->MB;
+            if (p->tau == 0) {
+                sane = sane && L <= p->max_seq;
+                if (!sane) flag(p->status, PA_CHECK_SEQ_LEN);
+            }
             if (sane && n > p->tau) items = p->Hkv * ((n + 2 * p->TT - 1) / (2 * p->TT));
         }
         incl = items;
@@ -1670,6 +1675,15 @@ int prefill_tau(const AttnArgs &a) {
     const int G = a.Hq / a.Hkv;
     // The tensor-core kernel takes the row max of unscaled scores: scale > 0.
     if ((a.D != 64 && a.D != 128) || G < 1 || G > prefill::kBM || !(a.scale > 0.f)) return INT_MAX;
+    // Block-scaled pools: short requests of many rows, enough of them to fill
+    // the GPU, are cheaper on the tensor cores too, whose tile takes 128 rows
+    // at the price of one (64 requests, 4 kv heads, tensor cores against 16-row
+    // items: 56-64 rows at 2000 keys 59 against 94 us at head_dim 64, 75 against
+    // 140 at 128; 28 rows at up to 2000 keys 46 against 43, 59 against 63; 24
+    // rows 50 against 46, 65 against 56).
+    if (a.k_bscales && a.max_q <= prefill::kTauDefault && (long long)a.T * G >= 30LL * a.R &&
+        (long long)a.R * a.Hkv >= num_sms())
+        return 0;
     return prefill::kTauDefault;
 }
 
@@ -1709,6 +1723,7 @@ static pa_status build(const AttnArgs &a, int tau, cudaStream_t stream, Params &
     prm.G = G;
     prm.TT = TT;
     prm.tau = tau;
+    prm.max_seq = a.max_seq;
     prm.qscale = a.scale * 1.4426950408889634f;
     prm.status = status_word();
     if (!prm.status) return PA_ERR_CUDA;
@@ -1767,7 +1782,7 @@ pa_status launch_prefill(const AttnArgs &a, int tau, cudaStream_t stream) {
     long long items = 0;
     const pa_status st = build(a, tau, stream, prm, items);
     if (st != PA_OK) return st;
-    return launch_kind(a, prm, items, num_sms(), false, stream);
+    return launch_kind(a, prm, items, num_sms(), a.pdl, stream);
 }
 
 // HBM-bound split-K work and tensor-bound prefill work side by side.  The

@@ -98,7 +98,11 @@ __device__ __forceinline__ uint2 recode8(const uint2 c, float mul) {
 // rows.  Every CTA scans the requests for the blocks each writes (as the
 // index build scans them), so a warp finds its block by a binary search and no
 // list is stored; consecutive warps take the kv heads of one block, whose
-// rows lie side by side.
+// rows lie side by side.  Three round trips to memory (lengths; rows and block
+// id; the old scale) bound small steps, one wave of four CTAs per SM the large
+// ones (64 registers hold a block's 16 rows): 256 single tokens at 8 x 128 in
+// 8 us, a 5000-token chunk beside 200 in 14 us (as graph replays, which take
+// 4 us empty; three, five or six CTAs per SM 15 us, more waves 14-16).
 template <typename T, int D>
 __global__ void __launch_bounds__(kScaledThreads, 4) cache_write_scaled_kernel(const ScaledWriteArgs a) {
     constexpr int kLanes = D / 8;            // lanes that share a row, 8 elements each
@@ -208,13 +212,21 @@ __global__ void __launch_bounds__(kScaledThreads, 4) cache_write_scaled_kernel(c
 // Read
 // ---------------------------------------------------------------------------
 
+// One warp per run of consecutive rows of the output: its lanes find the rows'
+// requests (a search 32 probes wide in row_start_loc, then one step per row)
+// and slots side by side, then walk the rows' 8-element units 32 at a time, K
+// and V together.  HBM-bound: 3 bytes an element from FP8 pools, two of them
+// written.  Two units of each in flight and six CTAs per SM, written with the
+// streaming hint: 262,664 rows of 8 x 128 in 266 us (6.07 TB/s, 89% of the copy
+// rate; four units and four CTAs 270, without the hint 273-276).
 constexpr int kReadRows = 8;    // rows a warp takes at a time, at most
-constexpr int kReadUnroll = 4;  // units of K and of V in flight per lane
+constexpr int kReadUnroll = 2;  // units of K and of V in flight per lane
+constexpr int kReadCtasPerSm = 6;
 
 // kPool 0: 16-bit pools (a copy); 1: E4M3 pools with one scale each; 2: E4M3
 // pools with a scale per (block, kv head).  A unit is 8 elements.
 template <typename T, int kPool>
-__global__ void __launch_bounds__(kScaledThreads, 4) cache_read_kernel(const CacheReadArgs a) {
+__global__ void __launch_bounds__(kScaledThreads, kReadCtasPerSm) cache_read_kernel(const CacheReadArgs a) {
     using Src = typename std::conditional<kPool == 0, uint4, uint2>::type;
     const int lane = threadIdx.x & 31;
     const float ks = kPool == 1 && a.k_scale ? *a.k_scale : 1.f;
@@ -311,11 +323,11 @@ __global__ void __launch_bounds__(kScaledThreads, 4) cache_read_kernel(const Cac
             for (int j = 0; j < kReadUnroll; ++j) {
                 if (to[j] < 0) continue;
                 if constexpr (kPool == 0) {
-                    ko[to[j]] = k[j];
-                    vo[to[j]] = v[j];
+                    __stcs(ko + to[j], k[j]);
+                    __stcs(vo + to[j], v[j]);
                 } else {
-                    ko[to[j]] = dequantize8<T>(k[j], kf[j]);
-                    vo[to[j]] = dequantize8<T>(v[j], vf[j]);
+                    __stcs(ko + to[j], dequantize8<T>(k[j], kf[j]));
+                    __stcs(vo + to[j], dequantize8<T>(v[j], vf[j]));
                 }
             }
         }
@@ -380,7 +392,7 @@ pa_status launch_cache_read(CacheReadArgs a, int pool, pa_dtype dtype, cudaStrea
     a.status = status_word();
     if (!a.status) return PA_ERR_CUDA;
     // Few rows: fewer a warp, down to one, until they fill the GPU once.
-    const long long cap = 4LL * num_sms();
+    const long long cap = (long long)kReadCtasPerSm * num_sms();
     a.rows_per_warp = kReadRows;
     while (a.rows_per_warp > 1 && (long long)a.N < cap * kScaledWarps * a.rows_per_warp) a.rows_per_warp /= 2;
     const int per_block = a.rows_per_warp * kScaledWarps;
