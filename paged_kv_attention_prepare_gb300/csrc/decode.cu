@@ -84,6 +84,7 @@ struct Params {
     const uint8_t *k_bscales;  // block-scaled E4M3 pools: [NB][Hkv] scale bytes
     const uint8_t *v_bscales;
     unsigned int *status;
+    int counter_dirty;    // host side: the item counter is not zeroed yet
     int launch_pdl;       // host side: the split-K grid as a programmatic dependent of the grid before
     int launch_part;      // host side: 0 split-K grid and merge pass, 1 the grid only, 2 the merge only
     int max_tokens;       // host side: most query tokens of a request handled here (at least 1)
@@ -1705,6 +1706,12 @@ pa_status launch_split_k(Params &prm, long long max_items, cudaStream_t stream) 
     }
     // Persistent grid: every resident slot once, no more CTAs than items.
     long long grid = (long long)per_sm * num_sms();
+    if (prm.counter_dirty) {
+        // An item per CTA at most: its own index, and no counter (a memset
+        // less: three requests of a few tokens, 10.2 -> 8.2 us).
+        if (max_items <= grid && !kGroups) prm.item_counter = nullptr;
+        else PA_TRY_CUDA(cudaMemsetAsync(prm.item_counter, 0, sizeof(unsigned int), stream));
+    }
     if (max_items < grid) grid = max_items;
     if (grid < 1) grid = 1;
     if (prm.launch_pdl) {
@@ -1892,6 +1899,7 @@ pa_status launch_decode(const AttnArgs &a, int tau, cudaStream_t stream) {
     const int max_n = a.max_q < tau ? a.max_q : tau;
     prm.max_tokens = max_n < 1 ? 1 : max_n > 64 ? 64 : max_n;
     prm.item_counter = a.ctrl ? a.ctrl + kCtrlDecodeCounter : nullptr;
+    prm.counter_dirty = a.ctrl_dirty ? 1 : 0;
     // Block-scaled pools, no request for the tensor-core kernel, and requests
     // of more than 8 rows on average: wide items.
     const bool wide = a.k_bscales && a.max_q <= tau && (long long)a.T * prm.G > 8LL * a.R;

@@ -93,9 +93,6 @@ using namespace pa;
 
 namespace {
 
-// Keys and values the split-K kernel reads in some 7 us.
-constexpr long long kFewSplitKBytes = 48LL << 20;
-
 // Checks and argument packing shared by both index-build entry points.
 pa_status check_prepare_core(const PrepArgs &a) {
     if (a.R < 0 || a.T < 0 || a.bs <= 0 || a.NB < 0 || a.MB < 0 || a.qsl_cap < a.R + 1)
@@ -601,28 +598,15 @@ static pa_status attention_checked(const void *q, const void *key_cache, const v
         }
     }
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (a.ctrl) PA_TRY_CUDA(cudaMemsetAsync(a.ctrl, 0, kCtrlWords * sizeof(unsigned int), st));
     const int tau = prefill_tau(a);
+    // Over block-scaled pools, a call for the split-K kernel alone zeroes its
+    // counter only when its items outnumber its CTAs.
+    a.ctrl_dirty = a.ctrl && k_scales && max_query_len <= tau;
+    if (a.ctrl && !a.ctrl_dirty)
+        PA_TRY_CUDA(cudaMemsetAsync(a.ctrl, 0, kCtrlWords * sizeof(unsigned int), st));
     a.pdl = false;
     a.decode_part = 0;
     if (tau == 0) return launch_prefill(a, tau, st);
-    // Block-scaled pools, and the short requests, if there are any, can hardly
-    // have work: the tensor-core kernel on the whole GPU, as a programmatic
-    // dependent of the split-K grid, whose CTAs then find nothing to do while
-    // it starts (five prompts of up to 1300 tokens, 16/16 heads, head_dim 64:
-    // 39 -> 35 us), and the merge pass last.
-    if (a.k_bscales && tau != INT_MAX && max_query_len > tau &&
-        (long long)(num_reqs - 1) * max_seq_len * 2 * num_kv_heads * head_dim <= kFewSplitKBytes) {
-        a.decode_part = 1;
-        pa_status r = launch_decode(a, tau, st);
-        if (r != PA_OK) return r;
-        a.pdl = true;
-        r = launch_prefill(a, tau, st);
-        if (r != PA_OK) return r;
-        a.pdl = false;
-        a.decode_part = 2;
-        return launch_decode(a, tau, st);
-    }
     // Both request classes possible: the two kernels side by side.
     if (a.ctrl && tau != INT_MAX && max_query_len > tau && num_reqs > 1)
         return launch_attention_overlapped(a, tau, st);

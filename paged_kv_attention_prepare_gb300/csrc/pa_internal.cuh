@@ -128,6 +128,7 @@ struct AttnArgs {
     void *pf_ws;           // the workspace past the decode partials (NULL: none)
     size_t pf_bytes;
     unsigned int *ctrl;    // control block at the workspace's start (NULL: none)
+    bool ctrl_dirty;       // its counters are not zeroed yet (launch_decode does, where it uses them)
     uint32_t flags;        // PA_ATTN_* bits
     bool pdl;              // launch the split-K kernel as a programmatic dependent
     int decode_part;       // launch_decode: 0 split-K grid + merge, 1 the grid only, 2 the merge only

@@ -1782,7 +1782,7 @@ pa_status launch_prefill(const AttnArgs &a, int tau, cudaStream_t stream) {
     long long items = 0;
     const pa_status st = build(a, tau, stream, prm, items);
     if (st != PA_OK) return st;
-    return launch_kind(a, prm, items, num_sms(), a.pdl, stream);
+    return launch_kind(a, prm, items, num_sms(), false, stream);
 }
 
 // HBM-bound split-K work and tensor-bound prefill work side by side.  The

@@ -487,6 +487,70 @@ def test_attention_mixed_batch(d):
     assert torch.equal(full, again)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g,new", [(8, (1, 2)), (3, (4, 6)), (5, (2, 5)), (16, (1, 1))])
+def test_attention_items_of_many_rows(d, g, new):
+    # short requests of 9 rows and more on average: items of 16 rows, some of
+    # their tiles empty, contexts of several partitions and of none
+    rng = np.random.default_rng(d + g)
+    old = np.array([0, 0, 3, 700, 1030, 2050, 4500, 15, 2047])
+    new = rng.integers(new[0], new[1], len(old), endpoint=True)
+    case = _case(d * g, new, old, 2 * g, 2, d, "bf16")
+    full = _check(case)
+    assert torch.equal(full, _check(case))
+    for ws in (None, 256, 60_000):
+        _check(case, workspace=ws)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_attention_many_short_requests_of_many_rows(d, dtype):
+    # 30 rows a request and enough requests to fill the GPU: the tensor-core
+    # kernel alone, single tokens included
+    rng = np.random.default_rng(d)
+    r = 48
+    new, old = rng.integers(1, 9, r), rng.integers(0, 300, r)
+    new[:3], old[:3] = 1, [0, 500, 127]
+    case = _case(d, new, old, 32, 4, d, dtype)
+    _check(case)
+    _check(case, workspace=None)
+    # ... which then checks the lengths too
+    q, pools, bt, qsl, lens = case
+    bad = lens.copy()
+    bad[5], bad[7] = 100_000, 0
+    out = _attend(q, [to_dev(a) for a in pools], bt, qsl, bad, 0.1, max_seq=600)
+    assert _flagged() == {"seq_len"}
+    rows = np.ones(q.shape[0], bool)
+    for i in (5, 7):
+        rows[qsl[i]:qsl[i + 1]] = False
+        assert torch.isnan(out[qsl[i]:qsl[i + 1]]).all()      # left as they were
+    want = ref.attention(ref.f64(q), *pools, bt, qsl, lens, 0.1)
+    ref.check_attention(ref.f64(out), *want, q.dtype, rows=rows)
+
+
+def test_attention_one_workspace_for_calls_of_all_sizes():
+    # calls that use the workspace's counters and calls that do not, in turn on
+    # one stream, with nothing cleared between them
+    cases = [_case(1, [1, 2], [3, 40], 4, 2, 64, "bf16"),
+             _case(2, [1] * 40, list(range(1000, 1400, 10)), 16, 4, 64, "bf16"),
+             _case(3, [200, 1], [10, 900], 8, 2, 64, "bf16"),
+             _case(4, [3] * 60, [30] * 60, 32, 4, 64, "bf16")]
+    ws = torch.full((64 << 20,), 0xFF, dtype=torch.uint8, device="cuda")
+    got = []
+    for i in (0, 1, 2, 3, 0, 2, 1, 0, 3):
+        q, pools, bt, qsl, lens = cases[i]
+        out = torch.full_like(q, float("nan"))
+        pa.pa_attention_scaled(q, *[to_dev(a) for a in pools], to_dev(bt), to_dev(qsl),
+                               to_dev(lens.astype(np.int32)), int(np.diff(qsl).max()),
+                               int(lens.max()), 0.125, out, ws)
+        got.append((i, out))
+    _ok()
+    for i, out in got:
+        q, pools, bt, qsl, lens = cases[i]
+        want = ref.attention(ref.f64(q), *pools, bt, qsl, lens, 0.125)
+        ref.check_attention(ref.f64(out), *want, q.dtype)
+
+
 @pytest.mark.parametrize("g", [2, 130])
 def test_attention_on_the_split_kernel_alone(g):
     # a scale that is not positive, and more heads a group than a tile's rows,
@@ -768,3 +832,81 @@ def test_pools_past_32_bit_offsets():
     assert torch.equal(ko.cpu(), torch.from_numpy(rows).bfloat16())
     del dev
     torch.cuda.empty_cache()
+
+
+def test_calls_on_a_given_stream():
+    # the stream argument: an object, a handle, and the current one
+    rng = np.random.default_rng(25)
+    pools = _pools(rng, 10, 2, 64)
+    bt, qsl, sl = np.array([[4, 7]], np.int32), _starts([20]), np.array([20], np.int32)
+    key, value, q = (_rows(rng, 20, h, 64, "bf16", 1.0) for h in (2, 2, 4))
+    args = [to_dev(a) for a in (bt, qsl, sl, np.zeros(1, np.int32))]
+    want = None
+    for how in ("object", "handle", "current"):
+        dev = [to_dev(a) for a in pools]
+        out = torch.full_like(q, float("nan"))
+        ko, vo = torch.empty_like(key), torch.empty_like(value)
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        kw = {"stream": side if how == "object" else side.cuda_stream if how == "handle" else None}
+        with torch.cuda.stream(side if how == "current" else torch.cuda.current_stream()):
+            pa.pa_cache_write_scaled(key, value, *dev, *args[:3], **kw)
+            pa.pa_attention_scaled(q, *dev, *args[:3], 20, 20, 0.125, out, **kw)
+            pa.pa_cache_read(dev[0], dev[1], args[0], args[3], args[1], ko, vo, k_scales=dev[2],
+                             v_scales=dev[3], **kw)
+        side.synchronize()
+        _ok()
+        got = [*dev, out, ko, vo]
+        if want is not None:
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        want = got
+
+
+def test_binding_refuses_tensors_that_do_not_fit():
+    z = lambda *s, dt=torch.uint8: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
+    i32, bf = torch.int32, torch.bfloat16
+    pools = [z(4, 16, 2, 64), z(4, 16, 2, 64), z(4, 2), z(4, 2)]
+    bt, qsl, sl = z(1, 2, dt=i32), z(2, dt=i32), z(1, dt=i32)
+    x, q = z(3, 2, 64, dt=bf), z(3, 4, 64, dt=bf)
+
+    def write(**kw):
+        a = dict(key=x, value=x, kc=pools[0], vc=pools[1], ks=pools[2], vs=pools[3], bt=bt, qsl=qsl,
+                 sl=sl)
+        a.update(kw)
+        pa.pa_cache_write_scaled(*a.values())
+
+    for kw in (dict(key=x.float()), dict(value=x.half()), dict(kc=pools[0].to(bf)),
+               dict(ks=pools[2].int()), dict(bt=bt.long()), dict(qsl=qsl.long()), dict(key=None)):
+        with pytest.raises(TypeError):
+            write(**kw)
+    for kw in (dict(key=x[:, :1]), dict(value=x[:2]), dict(key=x.transpose(0, 1)),
+               dict(vc=pools[1][:3]), dict(ks=z(4, 3)), dict(vs=z(2, 2)), dict(qsl=z(3, dt=i32)),
+               dict(bt=z(2, 2, dt=i32)), dict(sl=z(2, dt=i32)), dict(kc=pools[0][:, ::2]),
+               dict(key=z(3, 2, 128, dt=bf)[:, :, ::2])):
+        with pytest.raises(ValueError):
+            write(**kw)
+
+    def attend(**kw):
+        a = dict(q=q, kc=pools[0], vc=pools[1], ks=pools[2], vs=pools[3], bt=bt, qsl=qsl, sl=sl,
+                 max_q=3, max_seq=16, scale=1.0, out=torch.empty_like(q))
+        a.update(kw)
+        pa.pa_attention_scaled(*a.values())
+
+    for kw in (dict(out=q.float()), dict(q=q.float(), out=q.float()), dict(max_q="3"),
+               dict(scale=None), dict(kc=pools[0].to(bf), vc=pools[1].to(bf))):
+        with pytest.raises(TypeError):
+            attend(**kw)
+    for kw in (dict(kc=q, vc=q), dict(out=q[:2]), dict(q=q[:, :, :32], out=q[:, :, :32]), dict(max_seq=1 << 40),
+               dict(q=q.transpose(0, 1))):
+        with pytest.raises(ValueError):
+            attend(**kw)
+    with pytest.raises(pa.PAError) as e:
+        attend(q=z(3, 3, 64, dt=bf), out=z(3, 3, 64, dt=bf))          # 3 heads over 2
+    assert e.value.status == pa.PA_ERR_UNSUPPORTED
+    with pytest.raises(pa.PAError) as e:                              # tables beside a pool scale
+        pa.pa_cache_read(*pools[:2], bt, sl, qsl, x, x.clone(), k_scales=pools[2],
+                         v_scales=pools[3], k_scale=torch.ones(1, device="cuda"))
+    assert e.value.status == pa.PA_ERR_INVALID
+    with pytest.raises(TypeError):                                    # one table alone
+        pa.pa_cache_read(*pools[:2], bt, sl, qsl, x, x.clone(), k_scales=pools[2])
+    assert pa.pa_get_status() == (pa.PA_OK, 0)
