@@ -1684,6 +1684,18 @@ int prefill_tau(const AttnArgs &a) {
     if (a.k_bscales && a.max_q <= prefill::kTauDefault && (long long)a.T * G >= 30LL * a.R &&
         (long long)a.R * a.Hkv >= num_sms())
         return 0;
+    // A prompt by itself, or a few short contexts: one launch of this kernel
+    // for every request, rather than the two kernels side by side and a merge
+    // pass.  A short request then costs its (request, kv head) a tile's 2 us
+    // per 128 keys on one SM, so only where all of them could take some 11 us
+    // of the GPU (five prompts of up to 1300 tokens, 16/16 heads, head_dim 64:
+    // 38 -> 34 us; one of 75 tokens 18 -> 12; 828 tokens beside 11 single
+    // tokens at up to 954, 28/4 heads: 35 -> 25; at worst 15 single tokens at
+    // up to 1892 of one kv head: 28 -> 30).
+    if (a.k_bscales && a.max_q > prefill::kTauDefault) {
+        const long long tiles = ((long long)a.max_seq + prefill::kBN - 1) / prefill::kBN;
+        if (a.R == 1 || (tiles <= 16 && (long long)(a.R - 1) * a.Hkv * tiles <= 768)) return 0;
+    }
     return prefill::kTauDefault;
 }
 

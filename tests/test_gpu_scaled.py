@@ -474,16 +474,18 @@ def test_attention_chunks(d, dtype, g):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-def test_attention_mixed_batch(d):
-    # chunks beside short requests and single tokens: both kernels in one call
+@pytest.mark.parametrize("max_seq", [None, 4000])
+def test_attention_mixed_batch(d, max_seq):
+    # chunks beside short requests and single tokens: on the tensor-core kernel
+    # alone, or (contexts that may be long) on both kernels side by side
     new = np.array([1, 260, 1, 4, 40, 1, 16, 1])
     old = np.array([900, 130, 0, 15, 0, 1300, 64, 33])
     case = _case(d, new, old, 8, 2, d, "bf16")
-    full = _check(case)
+    full = _check(case, max_seq=max_seq)
     # any workspace is right: none, the counters alone, room for few partials
     for ws in (None, 256, 4096, 200_000):
-        _check(case, workspace=ws)
-    again = _check(case)
+        _check(case, workspace=ws, max_seq=max_seq)
+    again = _check(case, max_seq=max_seq)
     assert torch.equal(full, again)
 
 
@@ -740,19 +742,19 @@ def test_captured_step_replays_with_new_inputs():
     i32 = dict(dtype=torch.int32, device="cuda")
     bt, qsl, sl = torch.zeros(r, mb, **i32), torch.zeros(r + 1, **i32), torch.zeros(r, **i32)
     first, starts = torch.zeros(r, **i32), torch.zeros(r + 1, **i32)
-    tcap, ncap = 90, 1500
+    tcap, ncap, bound = 90, 1500, 4000           # bound on seq_lens: both kernels side by side
     bf = dict(dtype=torch.bfloat16, device="cuda")
     q, out = torch.zeros(tcap, hq, d, **bf), torch.zeros(tcap, hq, d, **bf)
     key, value = torch.zeros(tcap, hkv, d, **bf), torch.zeros(tcap, hkv, d, **bf)
     ko, vo = torch.zeros(ncap, hkv, d, **bf), torch.zeros(ncap, hkv, d, **bf)
     pools = _pools(rng, nb, hkv, d)
     dev = [to_dev(a) for a in pools]
-    ws = torch.empty(pa.pa_attention_workspace_size(r, tcap, tcap, mb * 16, hq, hkv, d),
+    ws = torch.empty(pa.pa_attention_workspace_size(r, tcap, tcap, bound, hq, hkv, d),
                      dtype=torch.uint8, device="cuda")
 
     def calls():
         pa.pa_cache_write_scaled(key, value, *dev, bt, qsl, sl)
-        pa.pa_attention_scaled(q, *dev, bt, qsl, sl, tcap, mb * 16, 0.125, out, ws)
+        pa.pa_attention_scaled(q, *dev, bt, qsl, sl, tcap, bound, 0.125, out, ws)
         pa.pa_cache_read(dev[0], dev[1], bt, first, starts, ko, vo, k_scales=dev[2],
                          v_scales=dev[3])
 
