@@ -49,7 +49,7 @@
 // weights w = 2^(s + ev - m), m the running max of s + ev, carry V's scale
 // into PV, and the row sum takes a page's weights times 2^-ev.  The producer
 // leaves these numbers for each page in shared memory, one copy per V stage.
-// 5000-token chunk at 2048, 32/8, head_dim 128: 377 us against 323 with one
+// 5000-token chunk at 2048, 32/8, head_dim 128: 371 us against 323 with one
 // scale per pool; the softmax warps' issue slots are the price (they share two
 // quarters of the SM with the widening warps, and 12 more instructions a page
 // are 15% of theirs).  Measured and not kept: bringing a tile's pages to one
@@ -163,8 +163,9 @@ enum {
     B_IEMPTY = B_IFULL + 4,       // [kQueue] entry read by every other warp
     B_SPLITREQ = B_IEMPTY + 4,    // [2] per slot: the MMA warp asks for P as bf16 pairs
     B_SPLITDONE = B_SPLITREQ + 2, // [2] per slot: P rewritten (one arrive per softmax warp)
-    B_PSCALE = B_SPLITDONE + 2,   // [2] per V stage: the tile's page scales written
-    B_COUNT = B_PSCALE + 2
+    B_COUNT = B_SPLITDONE + 2,
+    // [2] per V stage, block-scaled pools only: the tile's page scales written
+    B_PSCALE = B_COUNT
 };
 constexpr int kQueue = 4;         // items the producer may run ahead
 
@@ -302,6 +303,7 @@ struct Item {
     int r, g, mt, n, L, qstart;
 };
 
+template <bool BS>
 struct Walker {
     const Params *p;
     int rb;
@@ -321,9 +323,11 @@ struct Walker {
             L = p->seq_lens[r];
             bool sane = a >= 0 && b <= p->T && n >= 0 && L >= n &&
                         (L + kPage - 1) / kPage <= p->MB;
-            if (p->tau == 0) {
-                sane = sane && L <= p->max_seq;
-                if (!sane) flag(p->status, PA_CHECK_SEQ_LEN);
+            if constexpr (BS) {
+                if (p->tau == 0) {
+                    sane = sane && L <= p->max_seq;
+                    if (!sane) flag(p->status, PA_CHECK_SEQ_LEN);
+                }
             }
             if (sane && n > p->tau) items = p->Hkv * ((n + 2 * p->TT - 1) / (2 * p->TT));
         }
@@ -594,9 +598,13 @@ paged_prefill_kernel(const __grid_constant__ Params p) {
     unsigned char *sQ = base;                       // 2 tiles: slot A, slot B
     unsigned char *sK = sQ + 2 * C::kQBytes;        // 2 stages
     unsigned char *sV = sK + 2 * C::kTileBytes;     // kVSt stages
+    // Only as many barriers as the pools use: two more for every kind of pool
+    // made the compiler unroll their initialisation differently and spill
+    // elsewhere (bf16 pools, 5000-token chunk: 310 -> 335 us).
+    constexpr int kBars = B_COUNT + (BS ? 2 : 0);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sV + kVSt * C::kTileBytes);
     unsigned char *sL = base + C::kLandOffset;      // FP8 at head_dim 64: [K st0, K st1, V st0, V st1]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + B_COUNT);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *q_items = reinterpret_cast<volatile int *>(tmem_slot + 2);   // [kQueue]
     // bf16 pools: per V stage and key half, 1 when the half stayed bf16
@@ -604,7 +612,7 @@ paged_prefill_kernel(const __grid_constant__ Params p) {
     volatile int *split_fmt = v_fmt + 2 * 3;   // [2]: halves of the requested P rewrite
     // bf16 pools: per V stage, 1 when the tile came widened (no conversion)
     volatile int *v_src = split_fmt + 2;        // [3]
-    static_assert(B_COUNT * 8 + (2 + kQueue + 2 * 3 + 2 + 3) * 4 <= 512, "control block");
+    static_assert(kBars * 8 + (2 + kQueue + 2 * 3 + 2 + 3) * 4 <= 512, "control block");
     static_assert(!BS || F8, "block scales belong to FP8 pools");
     // block-scaled pools: [2 V stages][pages of a tile], K factor and V
     // exponent, then 2^-ev, each twice (the operands of packed arithmetic)
@@ -625,7 +633,7 @@ paged_prefill_kernel(const __grid_constant__ Params p) {
     }
     if (tid == 0) {
         *abort_flag = 0;
-        for (int i = 0; i < B_COUNT; ++i) {
+        for (int i = 0; i < kBars; ++i) {
             const bool per_warp = (i >= B_PFULL && i < B_PFULL + 2) || (i >= B_OFREE && i < B_OFREE + 2) ||
                                   (i >= B_SPLITDONE && i < B_SPLITDONE + 2);
             // FP8: Q/K/V full are signalled by the widening warps; bf16: V full
@@ -655,7 +663,7 @@ paged_prefill_kernel(const __grid_constant__ Params p) {
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    Walker walk;
+    Walker<BS> walk;
     walk.begin(&p, lane);
     Item it;
 
@@ -1162,17 +1170,21 @@ paged_prefill_kernel(const __grid_constant__ Params p) {
                         }
                         // four chains: of every fourth pair, or (block scales) of a page
                         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                        auto chain = [](int k) { return BS ? k >> 4 : (k >> 1) & 3; };
-    #pragma unroll
-                        for (int k = 0; k < 64; k += 2)
-                            m4[chain(k)] = fmaxf(m4[chain(k)],
-                                                 fmaxf(__uint_as_float(r[k]), __uint_as_float(r[k + 1])));
                         float mx;
                         if constexpr (BS) {
+    #pragma unroll
+                            for (int k = 0; k < 64; k += 2)
+                                m4[k >> 4] = fmaxf(m4[k >> 4],
+                                                   fmaxf(__uint_as_float(r[k]), __uint_as_float(r[k + 1])));
     #pragma unroll
                             for (int pg = 0; pg < 4; ++pg) m4[pg] = fmaf(m4[pg], sc[pg].x, sc[pg].z);
                             mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                         } else {
+    #pragma unroll
+                            for (int k = 0; k < 64; k += 2)
+                                m4[(k >> 1) & 3] =
+                                    fmaxf(m4[(k >> 1) & 3],
+                                          fmaxf(__uint_as_float(r[k]), __uint_as_float(r[k + 1])));
                             mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2.x;
                         }
                         const bool need = mx > m_ref + (BS ? kRescaleThresholdBS : kRescaleThreshold);
