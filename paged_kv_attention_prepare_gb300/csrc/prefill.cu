@@ -1692,9 +1692,13 @@ int prefill_tau(const AttnArgs &a) {
     // at the price of one (64 requests, 4 kv heads, tensor cores against 16-row
     // items: 56-64 rows at 2000 keys 59 against 94 us at head_dim 64, 75 against
     // 140 at 128; 28 rows at up to 2000 keys 46 against 43, 59 against 63; 24
-    // rows 50 against 46, 65 against 56).
+    // rows 50 against 46, 65 against 56).  A (request, kv head) is then one SM's
+    // work, so not where one request alone may be long (63 of 500 keys beside
+    // one of 4000: 64 against 56 us, one of 8000: 108 against 56, one of 32,000:
+    // 368 against 64; where all have 8000, 205 against 325).
+    const long long tiles = ((long long)a.max_seq + prefill::kBN - 1) / prefill::kBN;
     if (a.k_bscales && a.max_q <= prefill::kTauDefault && (long long)a.T * G >= 30LL * a.R &&
-        (long long)a.R * a.Hkv >= num_sms())
+        (long long)a.R * a.Hkv >= num_sms() && tiles <= 32)
         return 0;
     // A prompt by itself, or a few short contexts: one launch of this kernel
     // for every request, rather than the two kernels side by side and a merge
@@ -1704,10 +1708,11 @@ int prefill_tau(const AttnArgs &a) {
     // 38 -> 34 us; one of 75 tokens 18 -> 12; 828 tokens beside 11 single
     // tokens at up to 954, 28/4 heads: 35 -> 25; at worst 15 single tokens at
     // up to 1892 of one kv head: 28 -> 30).
-    if (a.k_bscales && a.max_q > prefill::kTauDefault) {
-        const long long tiles = ((long long)a.max_seq + prefill::kBN - 1) / prefill::kBN;
-        if (a.R == 1 || (tiles <= 16 && (long long)(a.R - 1) * a.Hkv * tiles <= 768)) return 0;
-    }
+    // The same for one request by itself of up to 64 tiles (max_q is a bound: it
+    // may be a single token in a call laid out for more).
+    if (a.k_bscales && a.max_q > prefill::kTauDefault &&
+        (a.R == 1 ? tiles <= 64 : tiles <= 16 && (long long)(a.R - 1) * a.Hkv * tiles <= 768))
+        return 0;
     return prefill::kTauDefault;
 }
 

@@ -145,8 +145,12 @@ __global__ void __launch_bounds__(kScaledThreads, 4) cache_write_scaled_kernel(c
             if (s_first[mid] <= u) lo = mid;
             else hi = mid - 1;
         }
+        // Starts that go back and forth can add up past 32 bits, and the search
+        // then end anywhere: nothing but a block of this request goes on.
+        const int j = u - s_first[lo];
+        if (j < 0 || j >= blocks_of(lo, false)) continue;
         const int q0 = a.qsl[lo], L = a.seq_lens[lo], p0 = L - (a.qsl[lo + 1] - q0);
-        const int logical = p0 / kPage + (u - s_first[lo]);
+        const int logical = p0 / kPage + j;
         const int first = max(p0, logical * kPage);              // first new position here
         const int cnt = min(L, logical * kPage + kPage) - first; // new rows here
         const int off = first - logical * kPage;                 // slots held by earlier tokens

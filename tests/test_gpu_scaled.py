@@ -215,6 +215,35 @@ def test_write_many_requests():
     _same(got, _write_ref(key, value, pools, bt, _starts(new), lens))
 
 
+def test_write_more_requests_than_the_plain_shared_memory_holds():
+    rng = np.random.default_rng(31)
+    n = 20_000
+    new = (rng.random(n) < 0.1).astype(int)
+    old = rng.integers(0, 20, n)
+    lens = old + new
+    bt, nb = ref.tables(rng, lens)
+    pools = _pools(rng, nb, 1, 64)
+    key, value = (_rows(rng, int(new.sum()), 1, 64, "fp16") for _ in range(2))
+    got = _write(key, value, pools, bt, _starts(new), lens)
+    _ok()
+    _same(got, _write_ref(key, value, pools, bt, _starts(new), lens))
+
+
+def test_write_starts_that_go_back_are_flagged():
+    # requests 0 and 2 both take tokens 0 .. 19, request 1 would take -20
+    rng = np.random.default_rng(32)
+    lens = np.array([20, 5, 33])
+    bt, nb = ref.tables(rng, lens)
+    pools = _pools(rng, nb, 2, 64)
+    key, value = (_rows(rng, 20, 2, 64, "bf16") for _ in range(2))
+    got = _write(key, value, pools, bt, np.array([0, 20, 0, 20], np.int32), lens)
+    assert _flagged() == {"seq_len"}
+    want = pools
+    for r in (0, 2):
+        want = _write_ref(key, value, want, bt[r:r + 1], np.array([0, 20]), lens[r:r + 1])
+    _same(got, want)
+
+
 def test_write_bad_blocks_and_lengths_are_flagged_and_skipped():
     rng = np.random.default_rng(14)
     new, old = np.array([4, 4, 4, 4, 4]), np.array([0, 14, 30, 0, 3])
@@ -633,6 +662,30 @@ def test_attention_padding_rows_are_left():
     assert torch.isnan(out[t:]).all()
     want = ref.attention(ref.f64(q), *pools, bt, qsl, lens, 0.125)
     ref.check_attention(ref.f64(out[:t]), *want, q.dtype)
+
+
+@pytest.mark.parametrize("max_seq", [600, 8000, 20_000])
+@pytest.mark.parametrize("max_q", [1, 8, 100])
+def test_attention_bounds_above_what_the_batch_holds(max_q, max_seq):
+    # one call laid out for more: the bounds choose the kernel, not the result
+    for new, old in (([1], [500]), ([1, 1, 1], [3, 40, 515])):
+        q, pools, bt, qsl, lens = _case(33, new, old, 8, 2, 64, "bf16")
+        t, extra = q.shape[0], 100 - q.shape[0]
+        wide = torch.cat([q, torch.full((extra, 8, 64), float("nan"), dtype=q.dtype, device="cuda")])
+        out = _attend(wide, [to_dev(a) for a in pools], bt, qsl, lens, 0.125, max_q=max_q,
+                      max_seq=max_seq)
+        _ok()
+        assert torch.isnan(out[t:]).all()
+        want = ref.attention(ref.f64(q), *pools, bt, qsl, lens, 0.125)
+        ref.check_attention(ref.f64(out[:t]), *want, q.dtype)
+
+
+@pytest.mark.parametrize("max_seq", [4096, 4097])
+def test_attention_many_rows_with_contexts_that_may_be_long(max_seq):
+    # both sides of the length up to which the tensor-core kernel takes them
+    rng = np.random.default_rng(34)
+    new, old = rng.integers(4, 9, 48), rng.integers(0, 300, 48)
+    _check(_case(34, new, old, 32, 4, 64, "bf16"), max_seq=max_seq)
 
 
 def test_attention_bad_blocks_and_lengths_are_flagged():
