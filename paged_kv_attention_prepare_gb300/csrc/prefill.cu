@@ -107,6 +107,7 @@ struct Params {
     int R, T, MB, NB, Hq, Hkv, G;
     int TT;         // query tokens per 128-row tile: floor(128 / G)
     int tau;        // requests with more than tau query tokens are handled here
+    int class_len;  // kByLength: a walk over the requests per this many tokens of context (0: one)
     int max_seq;    // tau 0 (no other kernel checks the lengths): the caller's bound on seq_lens
     float qscale;   // softmax scale * log2(e)
     const float *k_scale, *v_scale;   // FP8 pools (device scalars; NULL = 1)
@@ -297,18 +298,30 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
 // Work items: per request with more than tau tokens, Hkv x ceil(n/(2 TT))
 // tile pairs, ordered last pair first (the tile with the most keys), kv heads
 // interleaved.  Every warp walks the request list itself.
+//
+// Block-scaled pools at head_dim 64, a call that runs here alone: one walk per
+// class of context lengths, the longest first, since a long request last is
+// the call's tail (64 requests of 1-8 tokens at up to 2000 keys, 28/4 heads:
+// 51 -> 44.5 us; five prompts of up to 1300 tokens 35 -> 33).  At head_dim 128
+// the same few lines changed the compiled softmax for the worse (5000-token
+// chunk 371 -> 389 us, two other forms of them 393 and 398) and are left out.
 // ---------------------------------------------------------------------------
+constexpr int kWalkClasses = 4;
+// At most this many requests: a walk is a pass of every warp over the lengths,
+// and many requests even out by themselves.
+constexpr int kWalkClassReqs = 256;
 
 struct Item {
     int r, g, mt, n, L, qstart;
 };
 
-template <bool BS>
+template <bool BS, bool kByLength>
 struct Walker {
     const Params *p;
     int rb;
     long long base;  // items before the window
     int n, L, a, items, incl, total;
+    int lo, hi;      // kByLength: this walk takes context lengths in (lo, hi]
 
     __device__ void load(int lane) {
         const int r = rb + lane;
@@ -328,6 +341,7 @@ struct Walker {
                     sane = sane && L <= p->max_seq;
                     if (!sane) flag(p->status, PA_CHECK_SEQ_LEN);
                 }
+                if constexpr (kByLength) sane = sane && L > lo && L <= hi;
             }
             if (sane && n > p->tau) items = p->Hkv * ((n + 2 * p->TT - 1) / (2 * p->TT));
         }
@@ -343,13 +357,22 @@ struct Walker {
         p = params;
         rb = 0;
         base = 0;
+        if constexpr (kByLength) {
+            hi = INT_MAX;
+            lo = p->class_len ? p->max_seq - p->class_len : -1;
+        }
         load(lane);
     }
     __device__ bool find(long long i, int lane, Item &it) {
         while (i >= base + total) {
             base += total;
             rb += 32;
-            if (rb >= p->R) return false;
+            if (rb >= p->R) {
+                if (!kByLength || lo < 0) return false;
+                hi = lo;   // the next shorter class
+                lo = max(lo - p->class_len, -1);
+                rb = 0;
+            }
             load(lane);
         }
         const int li = (int)(i - base);
@@ -663,7 +686,7 @@ paged_prefill_kernel(const __grid_constant__ Params p) {
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    Walker<BS> walk;
+    Walker<BS, BS && D == 64> walk;
     walk.begin(&p, lane);
     Item it;
 
@@ -1691,8 +1714,9 @@ int prefill_tau(const AttnArgs &a) {
     // the GPU, are cheaper on the tensor cores too, whose tile takes 128 rows
     // at the price of one (64 requests, 4 kv heads, tensor cores against 16-row
     // items: 56-64 rows at 2000 keys 59 against 94 us at head_dim 64, 75 against
-    // 140 at 128; 28 rows at up to 2000 keys 46 against 43, 59 against 63; 24
-    // rows 50 against 46, 65 against 56).  A (request, kv head) is then one SM's
+    // 140 at 128; 28 rows at up to 2000 keys 40 against 45, 62 against 60, all at
+    // 2000 keys 59 against 57, 75 against 90; 21 rows 40 against 43, 62 against
+    // 56; 14 rows 42 against 31, 63 against 40).  A (request, kv head) is then one SM's
     // work, so not where one request alone may be long (63 of 500 keys beside
     // one of 4000: 64 against 56 us, one of 8000: 108 against 56, one of 32,000:
     // 368 against 64; where all have 8000, 205 against 325).
@@ -1758,6 +1782,9 @@ static pa_status build(const AttnArgs &a, int tau, cudaStream_t stream, Params &
     if (!prm.status) return PA_ERR_CUDA;
     // upper bound on the row tiles
     items = (long long)a.Hkv * ((long long)a.R + ((long long)a.T + 2 * TT - 1) / (2 * TT));
+    // (longest first only where a CTA takes more than one)
+    prm.class_len = a.k_bscales && tau == 0 && items > num_sms() && a.R > 1 && a.R <= kWalkClassReqs
+                        ? a.max_seq / kWalkClasses + 1 : 0;
     const bool bf16 = a.dtype == PA_BF16;
     // bf16 pools: the prefill requests' V widened once, into the workspace's
     // tail: [R] first tokens, then [pages][Hkv] flags, then the f16 rows.

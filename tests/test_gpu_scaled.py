@@ -559,6 +559,18 @@ def test_attention_many_short_requests_of_many_rows(d, dtype):
     ref.check_attention(ref.f64(out), *want, q.dtype, rows=rows)
 
 
+@pytest.mark.parametrize("r", [60, 256, 257])
+def test_attention_contexts_in_classes_of_length(r):
+    # the tensor-core kernel takes long contexts first: lengths on both sides of
+    # the classes' borders at 400 keys, and more requests than it does that for
+    rng = np.random.default_rng(r)
+    new = rng.integers(4, 7, r)
+    lens = rng.choice([7, 96, 97, 98, 198, 199, 299, 300, 399, 400], r)
+    lens[:2] = 400, 7
+    out = _check(_case(35, new, lens - new, 32, 4, 64, "bf16"), max_seq=400)
+    assert not torch.isnan(out).any()
+
+
 def test_attention_one_workspace_for_calls_of_all_sizes():
     # calls that use the workspace's counters and calls that do not, in turn on
     # one stream, with nothing cleared between them
