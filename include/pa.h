@@ -621,8 +621,11 @@ pa_status pa_copy_blocks_scaled(void *key_cache, void *value_cache, uint8_t *k_s
  * the weights 2^(t_j - m) enter the product with V's elements as f16, with 11
  * significant bits relative to the heaviest key, and everything else is
  * float32.  The matrix products run in f16 (E4M3 widens to it exactly; bf16 q
- * is rounded to f16, exact inside f16's range), on the same two kernels and by
- * the same rules as pa_attention.  Workspace as pa_attention
+ * is rounded to f16, exact inside f16's range), on the same two kernels as
+ * pa_attention.  Which of them serves a request goes by the call's sizes and
+ * bounds (a prompt by itself, a few short contexts, or short requests of many
+ * (token, q head) rows run on the tensor-core kernel alone); the definition
+ * and the data checks do not depend on it.  Workspace as pa_attention
  * (pa_attention_workspace_size), flags as pa_attention_ex.  Errors and data
  * checks as pa_attention_ex, plus PA_ERR_INVALID for a NULL scale table.
  */

@@ -1761,13 +1761,13 @@ pa_status launch_typed(Params &prm, long long max_items, long long merge_splits,
 }
 
 // Rows of a wide item: as many 8-row tiles as two CTAs' registers hold.
-constexpr int wide_rows(int D) { return 16; }
+constexpr int kWideRows = 16;
 
 template <typename TQ, typename TC, int D>
 pa_status dispatch_rpi(int rpi, Params &prm, long long grid, long long merge, bool groups,
                        cudaStream_t stream) {
     if constexpr (std::is_same<TC, Fp8Block>::value)
-        if (rpi > 8) return launch_typed<TQ, TC, D, wide_rows(D)>(prm, grid, merge, false, stream);
+        if (rpi > 8) return launch_typed<TQ, TC, D, kWideRows>(prm, grid, merge, false, stream);
     switch (rpi) {
         case 1: return launch_typed<TQ, TC, D, 1>(prm, grid, merge, groups, stream);
         case 2: return launch_typed<TQ, TC, D, 2>(prm, grid, merge, groups, stream);
@@ -1901,9 +1901,11 @@ pa_status launch_decode(const AttnArgs &a, int tau, cudaStream_t stream) {
     prm.item_counter = a.ctrl ? a.ctrl + kCtrlDecodeCounter : nullptr;
     prm.counter_dirty = a.ctrl_dirty ? 1 : 0;
     // Block-scaled pools, no request for the tensor-core kernel, and requests
-    // of more than 8 rows on average: wide items.
+    // of more than 8 rows on average: wide items (64 requests of 4 tokens at
+    // 2000 keys, 16/4 heads, head_dim 64: 66 -> 33 us; of 8 rows or fewer the
+    // second tile would be empty).
     const bool wide = a.k_bscales && a.max_q <= tau && (long long)a.T * prm.G > 8LL * a.R;
-    const int rpi = wide ? wide_rows(a.D) : rows_per_item(prm.G, a.max_q < tau ? a.max_q : tau);
+    const int rpi = wide ? kWideRows : rows_per_item(prm.G, a.max_q < tau ? a.max_q : tau);
 
     // Workspace: per-request metadata, then (m, l) and o partials.
     const size_t meta = round_up((size_t)a.R * 16);
