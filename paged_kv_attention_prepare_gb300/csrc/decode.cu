@@ -1896,8 +1896,10 @@ pa_status launch_decode(const AttnArgs &a, int tau, cudaStream_t stream) {
     if (!prm.status) return PA_ERR_CUDA;
     prm.launch_pdl = a.pdl ? 1 : 0;
     prm.launch_part = a.decode_part;
-    const int max_n = a.max_q < tau ? a.max_q : tau;
-    prm.max_tokens = max_n < 1 ? 1 : max_n > 64 ? 64 : max_n;
+    // Beside chunks max_q says nothing of the requests here, most of them single
+    // tokens then: no CTAs for more (5000-token chunk beside 200 decodes, 32/8
+    // heads: 693.4 us with them, 691.6 without).
+    prm.max_tokens = a.max_q > tau || a.max_q < 1 ? 1 : a.max_q > 64 ? 64 : a.max_q;
     prm.item_counter = a.ctrl ? a.ctrl + kCtrlDecodeCounter : nullptr;
     prm.counter_dirty = a.ctrl_dirty ? 1 : 0;
     // Block-scaled pools, no request for the tensor-core kernel, and requests
